@@ -227,7 +227,7 @@ def plain_prepare(s):
     if s["signs"] is not None:
         w = rotated(w, s["signs"])
     wg = w.view(c["n"], -1, 128)
-    scale = (wg.abs().amax(-1) / 7.0).to(torch.float16)
+    scale = (wg.abs().amax(-1) / 7.0).float().to(torch.float16)
     d = scale.double()[..., None]
     q = torch.where(d > 0, (wg / d).round().clamp(-8.0, 7.0), torch.zeros_like(wg))
     return {"codes": q.view(c["n"], c["k"]).to(torch.int8), "scales": scale}
@@ -347,6 +347,8 @@ def exact(case, seed):
         return {"y": torch.einsum("mk,nk->mn", x, w)}
     w = rotate(s["w"]) if c["signs"] else s["w"].double()
     wg = w.reshape(c["n"], c["k"] // 128, 128)
-    scale = (torch.maximum(wg.amax(-1), -wg.amin(-1)) / 7.0).to(torch.float16)
-    q = torch.round(wg / scale.double()[..., None].clamp(min=2.0 ** -24)).clamp(-8.0, 7.0)
+    # the scale's definition rounds twice, to 32 and then to 16 bits
+    scale = (torch.maximum(wg.amax(-1), -wg.amin(-1)) / 7.0).float().to(torch.float16)
+    q = torch.round(wg / scale.double()[..., None]).clamp(-8.0, 7.0)
+    q = torch.nan_to_num(q, nan=0.0) * (scale != 0)[..., None]
     return {"codes": q.reshape(c["n"], c["k"]).to(torch.int8), "scales": scale}
