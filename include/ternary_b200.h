@@ -87,6 +87,7 @@ typedef int tb_status;
 #define TB_ERR_CUDA 6      /* a CUDA call or launch failed                     */
 #define TB_ERR_WORKSPACE 7 /* workspace NULL or smaller than required          */
 #define TB_ERR_DEVICE 8    /* current device is not a B200-class sm_100 GPU    */
+#define TB_ERR_VALUE 9     /* a number that is no size is out of its range     */
 
 typedef int tb_format;
 #define TB_FMT_2BIT 0
@@ -99,6 +100,7 @@ typedef int tb_dtype;
 #define TB_FP32 2
 #define TB_INT8 3
 #define TB_INT32 4
+#define TB_E4M3 5 /* 8-bit float, 4 exponent and 3 mantissa bits, largest 448 */
 
 typedef int tb_path;
 #define TB_PATH_AUTO 0   /* choose by shape (what tb_ternary_linear does)       */
@@ -275,6 +277,100 @@ int tb_ternary_linear_path(tb_dtype xt, tb_format f, int64_t M, int64_t N, int64
 tb_status tb_ternary_linear_noalloc(const void* x, tb_dtype xt, const uint8_t* packed,
                                     const uint16_t* scales, int64_t M, int64_t N, int64_t K,
                                     const int8_t* signs, void* y, tb_dtype yt, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Beside the ternary layer: the RMS norm in front of a linear layer and a
+ * linear layer with 4-bit weights (for the layers of a ternary model that keep
+ * more bits).  The source pages have no counterpart of either; the definitions
+ * are this library's own.
+ *
+ * 8-bit values with scales: codes a (TB_INT8: -127..127, TB_E4M3) beside fp32
+ * scales [M, K / group], row-major, group = K (one a row) or 128 (one per 128
+ * consecutive values); a stands for a * scale.
+ * ------------------------------------------------------------------------ */
+
+/* RMS norm of the rows of x [M, K], with the residual's addition in front and
+ * the block rotation or a rounding to 8 bits behind, in one pass.
+ *   h : with residual, h = x + residual (one fp32 addition), rounded to rt and
+ *       stored in residual_out; the norm is of the rounded h.  Without (both
+ *       pointers NULL; one alone is TB_ERR_NULL), h = x and rt is ignored.
+ *   n : n_k = h_k * weight_k / sqrt(mean_k h_k^2 + eps), fp32.
+ *       weight : device [K], wt in {BF16, FP16, FP32}; NULL = all ones, wt
+ *       ignored.  eps > 0 and finite (else TB_ERR_VALUE).
+ *   signs : device [K] int8 (+-1), 8-byte aligned: n_b = H (d_b * n_b) / 32 in
+ *       every 1024-block, what tb_ternary_linear and tb_q4_linear with the same
+ *       signs would do first (so pass them NULL there); needs K % 1024 == 0.
+ *       NULL: no rotation.
+ *   y : device [M, K].  yt in {BF16, FP16, FP32}: n, y_scales NULL and
+ *       scale_group 0.  yt in {INT8, E4M3}: with Q = 127 or 448 and per group
+ *       scale = max|n| / Q, the code nearest n / scale (ties to even) into y
+ *       and the scale into y_scales.  scale_group = K, or 128 where K % 128 == 0
+ *       (else TB_ERR_SHAPE).  A group whose largest |n| is below 2^-100 is
+ *       stored as scale 0, codes 0.  A group that holds a NaN or an infinity
+ *       gets the scale NaN (codes 0 in INT8, NaN in E4M3).
+ * xt, rt in {BF16, FP16, FP32}.  Any K from 1 to TB_RMS_NORM_MAX_K; pointers
+ * need natural alignment (16 bytes and K % 8 == 0 are faster).  Sums are fp32
+ * and do not overflow: a row whose sum of squares does is summed scaled.
+ * y may be x (yt == xt), residual_out may be residual or x (same dtype); any
+ * other overlap is undefined.  No workspace.  `weight` and `signs` are layer
+ * constants in the sense of the conventions above. */
+#define TB_RMS_NORM_MAX_K 32768
+tb_status tb_rms_norm(const void* x, tb_dtype xt, const void* residual, void* residual_out, tb_dtype rt,
+                      const void* weight, tb_dtype wt, float eps, const int8_t* signs, int64_t M,
+                      int64_t K, void* y, tb_dtype yt, float* y_scales, int64_t scale_group,
+                      void* stream);
+
+/* 4-bit weights: q in -8..7, held as c = q + 8; byte i of a row holds k = 2i in
+ * bits 0-3 and k = 2i + 1 in bits 4-7, row stride K/2 bytes, every byte valid;
+ * one fp16 scale per 128 weights of a row in a separate [N, K/128] array, so
+ * w = scale * q.  4 + 16/128 = 4.125 bits per weight. */
+
+/* Bytes of packed 4-bit codes of an [N, K] matrix (scales excluded); 0 for
+ * N <= 0, K <= 0 or K % 128 != 0. */
+size_t tb_q4_packed_bytes(int64_t N, int64_t K);
+
+/* Pack int8 codes [N, K] (-8..7); any other value is packed as the nearer end
+ * of that range and, when d_invalid_count is non-NULL, adds 1 to it.  Sizes and
+ * alignment as tb_pack_ternary. */
+tb_status tb_q4_pack(const int8_t* codes, int64_t N, int64_t K, uint8_t* packed,
+                     uint32_t* d_invalid_count, void* stream);
+
+/* Unpack into int8 codes [N, K].  Sizes and alignment as tb_unpack_ternary. */
+tb_status tb_q4_unpack(const uint8_t* packed, int64_t N, int64_t K, int8_t* codes, void* stream);
+
+/* Producer side: dense w [N, K] (wt in {BF16, FP16, FP32}, finite, 4-byte
+ * aligned), folded with the rotation of `signs` (as in tb_prepare_weights;
+ * needs K % 1024 == 0) or, signs NULL, taken as it is (K % 128 == 0), rounded
+ * per 128-group: s = fp16(fp32(max|w'| / 7)), at most 8188;
+ * q = clip(rint(w' / s), -8, 7) (halves to even), 0 where s = 0.  Computed in
+ * fp64, with the exactness of tb_prepare_weights.  packed 16-byte aligned;
+ * packed and scales are written in full. */
+tb_status tb_q4_prepare_weights(const void* w, tb_dtype wt, const int8_t* signs, int64_t N, int64_t K,
+                                uint8_t* packed, uint16_t* scales, void* stream);
+
+/* Device workspace bytes tb_q4_linear needs for these sizes (any path, any
+ * dtype); 0 for invalid sizes. */
+size_t tb_q4_linear_workspace(int64_t M, int64_t N, int64_t K);
+
+/* y = x' W^T with 4-bit W.
+ *   x : device [M, K].  xt in {BF16, FP16}: x_scales NULL, x_group 0.  xt in
+ *       {INT8, E4M3}: codes of 8-bit values with scales, as tb_rms_norm writes
+ *       them: x_scales device fp32 [M, K / x_group], x_group = K or 128.
+ *   signs : as in tb_ternary_linear; NULL for an 8-bit x (TB_ERR_DTYPE).
+ *   scales : device [N, K/128] fp16 bits, finite, at most 8188 in size.
+ *   y : device [M, N], yt in {BF16, FP16, FP32}.
+ *   workspace : at least tb_q4_linear_workspace(M, N, K) bytes, 16-byte aligned;
+ *       contents on entry do not matter.  Must not be shared by calls in flight
+ *       at once.
+ * M >= 1, N >= 1, K % 128 == 0, K % 1024 == 0 with signs; x, packed and
+ * workspace 16-byte aligned, signs 8 (else TB_ERR_ALIGN).
+ * Accuracy: relative L2 error <= 2e-3 and per element <= 1e-2 * max|s| * 8 *
+ * ||x_m||_2 before y's own rounding (the figures of tb_ternary_linear, w being
+ * up to 8 s here). */
+tb_status tb_q4_linear(const void* x, tb_dtype xt, const float* x_scales, int64_t x_group,
+                       const uint8_t* packed, const uint16_t* scales, int64_t M, int64_t N, int64_t K,
+                       const int8_t* signs, void* y, tb_dtype yt, void* workspace, size_t ws_bytes,
+                       void* stream);
 
 /* Read, and with clear != 0 reset, the fault word of the current device.  Every
  * wait inside the library's kernels is bounded; a wait that gives up (a

@@ -14,9 +14,9 @@ import re
 from . import build as _build
 
 TB_OK, TB_ERR_NULL, TB_ERR_SHAPE, TB_ERR_DTYPE, TB_ERR_FORMAT = 0, 1, 2, 3, 4
-TB_ERR_ALIGN, TB_ERR_CUDA, TB_ERR_WORKSPACE, TB_ERR_DEVICE = 5, 6, 7, 8
+TB_ERR_ALIGN, TB_ERR_CUDA, TB_ERR_WORKSPACE, TB_ERR_DEVICE, TB_ERR_VALUE = 5, 6, 7, 8, 9
 TB_FMT_2BIT, TB_FMT_BASE3, TB_FMT_1BIT = 0, 1, 2
-TB_BF16, TB_FP16, TB_FP32, TB_INT8, TB_INT32 = 0, 1, 2, 3, 4
+TB_BF16, TB_FP16, TB_FP32, TB_INT8, TB_INT32, TB_E4M3 = 0, 1, 2, 3, 4, 5
 TB_PATH_AUTO, TB_PATH_GEMV, TB_PATH_GEMM, TB_PATH_SIMPLE, TB_PATH_GEMV_TC = 0, 1, 2, 3, 4
 
 FORMATS = {"2bit": TB_FMT_2BIT, "base3": TB_FMT_BASE3, "1bit": TB_FMT_1BIT}
@@ -24,6 +24,7 @@ FORMATS = {"2bit": TB_FMT_2BIT, "base3": TB_FMT_BASE3, "1bit": TB_FMT_1BIT}
 HEADER = os.path.join(_build.ROOT, "include", "ternary_b200.h")
 
 _vp, _i64, _int, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+_f32 = ctypes.c_float
 _SIGNATURES = {
     "tb_status_string": (ctypes.c_char_p, [_int]),
     "tb_version": (_int, []),
@@ -42,6 +43,14 @@ _SIGNATURES = {
     "tb_test_stall_copies": (_int, [ctypes.c_uint32, ctypes.c_uint64]),
     "tb_ternary_linear_noalloc": (_int, [_vp, _int, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _int,
                                          _vp]),
+    "tb_rms_norm": (_int, [_vp, _int, _vp, _vp, _int, _vp, _int, _f32, _vp, _i64, _i64, _vp, _int, _vp, _i64,
+                           _vp]),
+    "tb_q4_packed_bytes": (_sz, [_i64, _i64]),
+    "tb_q4_pack": (_int, [_vp, _i64, _i64, _vp, _vp, _vp]),
+    "tb_q4_unpack": (_int, [_vp, _i64, _i64, _vp, _vp]),
+    "tb_q4_prepare_weights": (_int, [_vp, _int, _vp, _i64, _i64, _vp, _vp, _vp]),
+    "tb_q4_linear_workspace": (_sz, [_i64, _i64, _i64]),
+    "tb_q4_linear": (_int, [_vp, _int, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _int, _vp, _sz, _vp]),
 }
 
 _LIB = None
@@ -101,7 +110,7 @@ def _fmt(f):
 def dtype_code(t) -> int:
     import torch
     m = {torch.bfloat16: TB_BF16, torch.float16: TB_FP16, torch.float32: TB_FP32,
-         torch.int8: TB_INT8, torch.int32: TB_INT32}
+         torch.int8: TB_INT8, torch.int32: TB_INT32, torch.float8_e4m3fn: TB_E4M3}
     return m[t]
 
 
@@ -181,6 +190,47 @@ def tb_ternary_linear_noalloc(x, xt, packed, scales, m, n, k, signs, y, yt, stre
     st = load().tb_ternary_linear_noalloc(_ptr(x), xt, _ptr(packed), _ptr(scales), m, n, k,
                                           _ptr(signs), _ptr(y), yt, _stream(stream))
     return _done(st, "tb_ternary_linear_noalloc", check)
+
+
+TB_RMS_NORM_MAX_K = 32768
+
+
+def tb_rms_norm(x, xt, residual, residual_out, rt, weight, wt, eps, signs, m, k, y, yt, y_scales=None,
+                scale_group=0, stream=None, check=True):
+    st = load().tb_rms_norm(_ptr(x), xt, _ptr(residual), _ptr(residual_out), rt, _ptr(weight), wt, eps,
+                            _ptr(signs), m, k, _ptr(y), yt, _ptr(y_scales), scale_group, _stream(stream))
+    return _done(st, "tb_rms_norm", check)
+
+
+def tb_q4_packed_bytes(n: int, k: int) -> int:
+    return load().tb_q4_packed_bytes(n, k)
+
+
+def tb_q4_pack(codes, n, k, packed, invalid=None, stream=None, check=True):
+    st = load().tb_q4_pack(_ptr(codes), n, k, _ptr(packed), _ptr(invalid), _stream(stream))
+    return _done(st, "tb_q4_pack", check)
+
+
+def tb_q4_unpack(packed, n, k, codes, stream=None, check=True):
+    st = load().tb_q4_unpack(_ptr(packed), n, k, _ptr(codes), _stream(stream))
+    return _done(st, "tb_q4_unpack", check)
+
+
+def tb_q4_prepare_weights(w, wt, signs, n, k, packed, scales, stream=None, check=True):
+    st = load().tb_q4_prepare_weights(_ptr(w), wt, _ptr(signs), n, k, _ptr(packed), _ptr(scales),
+                                      _stream(stream))
+    return _done(st, "tb_q4_prepare_weights", check)
+
+
+def tb_q4_linear_workspace(m, n, k) -> int:
+    return load().tb_q4_linear_workspace(m, n, k)
+
+
+def tb_q4_linear(x, xt, x_scales, x_group, packed, scales, m, n, k, signs, y, yt, workspace, ws_bytes,
+                 stream=None, check=True):
+    st = load().tb_q4_linear(_ptr(x), xt, _ptr(x_scales), x_group, _ptr(packed), _ptr(scales), m, n, k,
+                             _ptr(signs), _ptr(y), yt, _ptr(workspace), ws_bytes, _stream(stream))
+    return _done(st, "tb_q4_linear", check)
 
 
 def tb_get_device_fault(clear=False) -> int:

@@ -56,6 +56,45 @@ __device__ __forceinline__ __half pw_double_to_half_rn(double a) {
   return __float2half_rn(static_cast<float>(r));
 }
 
+// The 1024-block at src folded with the rotation (w'_b = H (d_b * w_b) / 32):
+// lane a gets the elements 32 a .. 32 a + 31.  Called by a whole warp; xb is
+// 512 doubles of shared memory of its own.
+template <typename TIn>
+__device__ __forceinline__ void pw_load_folded(const TIn* __restrict__ src, const int8_t* __restrict__ sg, double* xb,
+                                               int lane, double (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const double f = static_cast<double>(to_f32<TIn>(src[32 * i + lane]));
+    v[i] = sg[32 * i + lane] < 0 ? -f : f;
+  }
+  pw_fwht32(v);  // over the high five index bits (r)
+  double u[32];
+#pragma unroll
+  for (int hf = 0; hf < 2; ++hf) {
+    // row r of this half, element c = lane: 16-byte chunk lane/2 stored at
+    // chunk (lane/2) ^ r
+#pragma unroll
+    for (int r = 0; r < 16; ++r) xb[32 * r + ((((lane >> 1) ^ r) & 15) << 1) + (lane & 1)] = v[16 * hf + r];
+    __syncwarp();
+    if ((lane >> 4) == hf) {
+      const int r = lane & 15;
+      const double2* rowp = reinterpret_cast<const double2*>(xb + 32 * r);
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        const double2 t = rowp[q ^ r];
+        u[2 * q] = t.x;
+        u[2 * q + 1] = t.y;
+      }
+    }
+    __syncwarp();
+  }
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = u[i];
+  pw_fwht32(v);  // over the low five index bits (c)
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] *= 0.03125;  // 1/32: exact
+}
+
 // kFmt: 0 = 2-bit slots, 1 = base-3.  grid (K / 1024, ceil(N / kPwWarps)).
 template <typename TIn, int kFmt>
 __global__ void __launch_bounds__(32 * kPwWarps)
@@ -71,39 +110,7 @@ __global__ void __launch_bounds__(32 * kPwWarps)
   const TIn* src = w + row * K + static_cast<int64_t>(blk) * kHB;
   double v[32];
   if (signs != nullptr) {
-    const int8_t* sg = signs + static_cast<int64_t>(blk) * kHB;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const double f = static_cast<double>(to_f32<TIn>(src[32 * i + lane]));
-      v[i] = sg[32 * i + lane] < 0 ? -f : f;
-    }
-    pw_fwht32(v);  // over the high five index bits (r)
-    double u[32];
-    double* xb = xbuf[warp];
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      // row r of this half, element c = lane: 16-byte chunk lane/2 stored at
-      // chunk (lane/2) ^ r
-#pragma unroll
-      for (int r = 0; r < 16; ++r) xb[32 * r + ((((lane >> 1) ^ r) & 15) << 1) + (lane & 1)] = v[16 * hf + r];
-      __syncwarp();
-      if ((lane >> 4) == hf) {
-        const int r = lane & 15;
-        const double2* rowp = reinterpret_cast<const double2*>(xb + 32 * r);
-#pragma unroll
-        for (int q = 0; q < 16; ++q) {
-          const double2 t = rowp[q ^ r];
-          u[2 * q] = t.x;
-          u[2 * q + 1] = t.y;
-        }
-      }
-      __syncwarp();
-    }
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = u[i];
-    pw_fwht32(v);  // over the low five index bits (c)
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] *= 0.03125;  // 1/32: exact
+    pw_load_folded<TIn>(src, signs + static_cast<int64_t>(blk) * kHB, xbuf[warp], lane, v);
   } else {
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = static_cast<double>(to_f32<TIn>(src[32 * lane + i]));

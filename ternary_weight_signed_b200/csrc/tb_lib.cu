@@ -21,7 +21,10 @@
 #include "gemv_b3.cuh"
 #include "gemv_tc.cuh"
 #include "hadamard.cuh"
+#include "norm.cuh"
 #include "pack.cuh"
+#include "q4.cuh"
+#include "q4_linear.cuh"
 #include "simple.cuh"
 
 namespace {
@@ -138,7 +141,8 @@ int dtype_size(int t) {
     case TB_FP16: return 2;
     case TB_FP32:
     case TB_INT32: return 4;
-    case TB_INT8: return 1;
+    case TB_INT8:
+    case TB_E4M3: return 1;
     default: return 0;
   }
 }
@@ -1096,6 +1100,71 @@ tb_status linear_impl(const LinearArgs& a, int path) {
   }
 }
 
+// ------------------------------------------------------------------ 4-bit linear
+struct Q4Args {
+  const void* x;
+  int xt;
+  const float* x_scales;
+  int64_t x_group;
+  const uint8_t* packed;
+  const uint16_t* scales;
+  int64_t M, N, K;
+  const int8_t* signs;
+  void* y;
+  int yt;
+  void* ws;
+  size_t ws_bytes;
+  cudaStream_t st;
+};
+
+bool is_8bit_dtype(int t) { return t == TB_INT8 || t == TB_E4M3; }
+
+size_t q4_required_ws(int64_t M, int64_t K) {
+  return (static_cast<size_t>(4) * static_cast<size_t>(M) * static_cast<size_t>(K) + 255) & ~static_cast<size_t>(255);
+}
+
+bool q4_sizes_ok(int64_t M, int64_t N, int64_t K) {
+  return M >= 1 && N >= 1 && K >= 128 && K % 128 == 0 && M <= kMaxDim && N < (int64_t(1) << 30) && K <= kMaxDim &&
+         M * K <= (int64_t(1) << 40) && N * K <= (int64_t(1) << 44);
+}
+
+tb_status validate_q4(const Q4Args& a) {
+  if (a.x == nullptr || a.packed == nullptr || a.scales == nullptr || a.y == nullptr) return TB_ERR_NULL;
+  const bool x8 = is_8bit_dtype(a.xt);
+  if (!x8 && a.xt != TB_BF16 && a.xt != TB_FP16) return TB_ERR_DTYPE;
+  if (!is_float_dtype(a.yt)) return TB_ERR_DTYPE;
+  if (x8 && a.x_scales == nullptr) return TB_ERR_NULL;
+  if (x8 ? a.signs != nullptr : a.x_scales != nullptr) return TB_ERR_DTYPE;
+  if (!q4_sizes_ok(a.M, a.N, a.K) || (a.signs != nullptr && a.K % 1024 != 0)) return TB_ERR_SHAPE;
+  if (x8 ? (a.x_group != a.K && a.x_group != 128) : a.x_group != 0) return TB_ERR_SHAPE;
+  if (!aligned(a.x, 16) || !aligned(a.packed, 16) || !aligned(a.scales, 2) || !aligned(a.y, dtype_size(a.yt)) ||
+      (a.signs != nullptr && !aligned(a.signs, 8)) || (x8 && !aligned(a.x_scales, 4)))
+    return TB_ERR_ALIGN;
+  if (a.ws == nullptr || a.ws_bytes < q4_required_ws(a.M, a.K)) return TB_ERR_WORKSPACE;
+  if (!aligned(a.ws, 16)) return TB_ERR_ALIGN;
+  return TB_OK;
+}
+
+tb_status run_q4(const Q4Args& a) {
+  float* xf = static_cast<float*>(a.ws);
+  if (a.signs != nullptr) {
+    const dim3 pg(static_cast<unsigned>(a.M), static_cast<unsigned>(a.K / kHB));
+    if (a.xt == TB_BF16)
+      prep_store_kernel<__nv_bfloat16, float><<<pg, kHThreads, 0, a.st>>>(static_cast<const __nv_bfloat16*>(a.x),
+                                                                          a.signs, xf, a.K);
+    else
+      prep_store_kernel<__half, float><<<pg, kHThreads, 0, a.st>>>(static_cast<const __half*>(a.x), a.signs, xf, a.K);
+  } else {
+    const int64_t n = a.M * a.K;
+    q4_convert_kernel<<<static_cast<unsigned>((n + 255) / 256), 256, 0, a.st>>>(
+        a.x, a.xt, a.x_scales, static_cast<int>(a.x_group), xf, n, static_cast<int>(a.K));
+  }
+  if (launch_status() != TB_OK) return TB_ERR_CUDA;
+  q4_linear_kernel<<<static_cast<unsigned>((a.N + kQ4Warps - 1) / kQ4Warps), 32 * kQ4Warps, 0, a.st>>>(
+      xf, a.packed, a.scales, a.y, a.yt, a.M, a.N, static_cast<int>(a.K));
+  return launch_status();
+}
+
 }  // namespace
 
 // =================================================================== C ABI
@@ -1112,6 +1181,7 @@ const char* tb_status_string(tb_status st) {
     case TB_ERR_CUDA: return "cuda error";
     case TB_ERR_WORKSPACE: return "workspace missing or too small";
     case TB_ERR_DEVICE: return "device is not sm_100";
+    case TB_ERR_VALUE: return "bad value";
     default: return "unknown status";
   }
 }
@@ -1332,6 +1402,114 @@ tb_status tb_ternary_linear_noalloc(const void* x, tb_dtype xt, const uint8_t* p
   a.ws_bytes = TB_NOALLOC_SCRATCH_BYTES;
   if (!gemv_ok(a)) return TB_ERR_SHAPE;
   return run_gemv(a, d);
+}
+
+tb_status tb_rms_norm(const void* x, tb_dtype xt, const void* residual, void* residual_out, tb_dtype rt,
+                      const void* weight, tb_dtype wt, float eps, const int8_t* signs, int64_t M, int64_t K,
+                      void* y, tb_dtype yt, float* y_scales, int64_t scale_group, void* stream) {
+  if (x == nullptr || y == nullptr || (residual == nullptr) != (residual_out == nullptr)) return TB_ERR_NULL;
+  const bool y8 = is_8bit_dtype(yt);
+  if (!is_float_dtype(xt) || (residual != nullptr && !is_float_dtype(rt)) ||
+      (weight != nullptr && !is_float_dtype(wt)) || (!y8 && !is_float_dtype(yt)))
+    return TB_ERR_DTYPE;
+  if (y8 && y_scales == nullptr) return TB_ERR_NULL;
+  if (!y8 && y_scales != nullptr) return TB_ERR_DTYPE;
+  if (M < 1 || K < 1 || M > kMaxDim || K > TB_RMS_NORM_MAX_K || (signs != nullptr && K % 1024 != 0))
+    return TB_ERR_SHAPE;
+  if (y8 ? (scale_group != K && !(scale_group == 128 && K % 128 == 0)) : scale_group != 0) return TB_ERR_SHAPE;
+  if (!(eps > 0.f) || !std::isfinite(eps)) return TB_ERR_VALUE;
+  if ((x == y && xt != yt) || (residual_out == x && xt != rt)) return TB_ERR_DTYPE;
+  if (!aligned(x, dtype_size(xt)) || !aligned(y, dtype_size(yt)) || (signs != nullptr && !aligned(signs, 8)) ||
+      (residual != nullptr && (!aligned(residual, dtype_size(rt)) || !aligned(residual_out, dtype_size(rt)))) ||
+      (weight != nullptr && !aligned(weight, dtype_size(wt))) || (y8 && !aligned(y_scales, 4)))
+    return TB_ERR_ALIGN;
+  const DevInfo* d = nullptr;
+  const tb_status st = current_device(&d);
+  if (st != TB_OK) return st;
+  NormParams p{x, residual, residual_out, weight, signs, y, y_scales, K, static_cast<int>(scale_group),
+               xt, rt, wt, yt, eps};
+  if (allow_smem(rms_norm_kernel, d) != TB_OK) return TB_ERR_CUDA;
+  rms_norm_kernel<<<static_cast<unsigned>(M), kNormThreads, static_cast<size_t>(4 * K), as_stream(stream)>>>(p);
+  return launch_status();
+}
+
+size_t tb_q4_packed_bytes(int64_t N, int64_t K) {
+  if (N <= 0 || K <= 0 || K % 128 != 0) return 0;
+  return static_cast<size_t>(N) * static_cast<size_t>(K / 2);
+}
+
+tb_status tb_q4_pack(const int8_t* codes, int64_t N, int64_t K, uint8_t* packed, uint32_t* d_invalid_count,
+                     void* stream) {
+  if (codes == nullptr || packed == nullptr) return TB_ERR_NULL;
+  if (!q4_sizes_ok(1, N, K) || N * K / 16 / 256 >= kMaxDim) return TB_ERR_SHAPE;
+  if (!aligned(codes, 16) || !aligned(packed, 16) || (d_invalid_count != nullptr && !aligned(d_invalid_count, 4)))
+    return TB_ERR_ALIGN;
+  const DevInfo* d = nullptr;
+  const tb_status st = current_device(&d);
+  if (st != TB_OK) return st;
+  const int64_t n = N * K / 16;
+  q4_pack_kernel<<<static_cast<unsigned>((n + 255) / 256), 256, 0, as_stream(stream)>>>(
+      reinterpret_cast<const int4*>(codes), reinterpret_cast<uint2*>(packed), n, d_invalid_count);
+  return launch_status();
+}
+
+tb_status tb_q4_unpack(const uint8_t* packed, int64_t N, int64_t K, int8_t* codes, void* stream) {
+  if (codes == nullptr || packed == nullptr) return TB_ERR_NULL;
+  if (!q4_sizes_ok(1, N, K) || N * K / 16 / 256 >= kMaxDim) return TB_ERR_SHAPE;
+  if (!aligned(codes, 16) || !aligned(packed, 16)) return TB_ERR_ALIGN;
+  const DevInfo* d = nullptr;
+  const tb_status st = current_device(&d);
+  if (st != TB_OK) return st;
+  const int64_t n = N * K / 16;
+  q4_unpack_kernel<<<static_cast<unsigned>((n + 255) / 256), 256, 0, as_stream(stream)>>>(
+      reinterpret_cast<const uint2*>(packed), reinterpret_cast<int4*>(codes), n);
+  return launch_status();
+}
+
+tb_status tb_q4_prepare_weights(const void* w, tb_dtype wt, const int8_t* signs, int64_t N, int64_t K,
+                                uint8_t* packed, uint16_t* scales, void* stream) {
+  if (w == nullptr || packed == nullptr || scales == nullptr) return TB_ERR_NULL;
+  if (!is_float_dtype(wt)) return TB_ERR_DTYPE;
+  if (!q4_sizes_ok(1, N, K) || (signs != nullptr && K % 1024 != 0)) return TB_ERR_SHAPE;
+  const int64_t blocks = (K + kHB - 1) / kHB * ((N + kPwWarps - 1) / kPwWarps);
+  if (blocks > kMaxDim) return TB_ERR_SHAPE;
+  if (!aligned(w, 4) || !aligned(packed, 16) || !aligned(scales, 2) || (signs != nullptr && !aligned(signs, 8)))
+    return TB_ERR_ALIGN;
+  const DevInfo* d = nullptr;
+  const tb_status st = current_device(&d);
+  if (st != TB_OK) return st;
+  const cudaStream_t s = as_stream(stream);
+  const unsigned grid = static_cast<unsigned>(blocks);
+  const int block = 32 * kPwWarps, k = static_cast<int>(K);
+  switch (wt) {
+    case TB_BF16:
+      q4_prepare_kernel<<<grid, block, 0, s>>>(static_cast<const __nv_bfloat16*>(w), signs, packed, scales, N, k);
+      break;
+    case TB_FP16:
+      q4_prepare_kernel<<<grid, block, 0, s>>>(static_cast<const __half*>(w), signs, packed, scales, N, k);
+      break;
+    default:
+      q4_prepare_kernel<<<grid, block, 0, s>>>(static_cast<const float*>(w), signs, packed, scales, N, k);
+      break;
+  }
+  return launch_status();
+}
+
+size_t tb_q4_linear_workspace(int64_t M, int64_t N, int64_t K) {
+  return q4_sizes_ok(M, N, K) ? q4_required_ws(M, K) : 0;
+}
+
+tb_status tb_q4_linear(const void* x, tb_dtype xt, const float* x_scales, int64_t x_group, const uint8_t* packed,
+                       const uint16_t* scales, int64_t M, int64_t N, int64_t K, const int8_t* signs, void* y,
+                       tb_dtype yt, void* workspace, size_t ws_bytes, void* stream) {
+  const Q4Args a{x, xt, x_scales, x_group, packed, scales, M, N, K, signs, y, yt, workspace, ws_bytes,
+                 as_stream(stream)};
+  tb_status st = validate_q4(a);
+  if (st != TB_OK) return st;
+  const DevInfo* d = nullptr;
+  st = current_device(&d);
+  if (st != TB_OK) return st;
+  return run_q4(a);
 }
 
 tb_status tb_test_stall_copies(uint32_t stall, uint64_t wait_limit_ns) {

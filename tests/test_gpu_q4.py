@@ -1,0 +1,362 @@
+"""GPU parity of the 4-bit linear layer: tb_q4_pack / unpack / prepare_weights
+bit for bit, tb_q4_linear against its definition in float64
+(oracle/q4_norm_oracle.py), and the chain norm -> 8 bits -> linear.
+
+Tolerances of the linear layer, counted in roundings before the first run.
+Up to 16 tokens without a rotation every product is exact and only fp32 sums
+round: a chain of at most 160 additions whose partial sums grow to
+T = sum |w| |x| is off by less than 160 / 2 * 2^-24 T < 2^-17 T (a tensor core
+may cut instead of round: 8 sums of a 128-group, twice as much each).  In every
+other call a weight and, where x is rotated, x' are also rounded to 11 bits:
+independent errors of 2^-11 / sqrt(3) rms each at most, so at most
+2^-11 * sqrt(2/3) < 2^-11 of y in relative L2 over a whole output, and at most
+2^-10 T for one.  y's own type adds eps / 2 of each value."""
+import functools
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import q4_norm_oracle as q4o
+from ternary_weight_signed_b200 import binding as tb
+from tests.gpu_util import DEV, ensure_lib
+
+pytestmark = pytest.mark.gpu
+
+T = {"bf16": (tb.TB_BF16, torch.bfloat16), "fp16": (tb.TB_FP16, torch.float16), "fp32": (tb.TB_FP32, torch.float32),
+     "int8": (tb.TB_INT8, torch.int8), "e4m3": (tb.TB_E4M3, torch.float8_e4m3fn)}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    ensure_lib()
+    tb.tb_get_device_fault(clear=True)
+    yield
+    assert tb.tb_get_device_fault() == 0
+
+
+def draw_signs(rng, k):
+    return torch.from_numpy(rng.choice([-1, 1], k).astype(np.int8))
+
+
+# ------------------------------------------------------------------ weights
+@pytest.mark.parametrize("n,k", [(1, 128), (3, 384), (301, 1024), (5, 5120)])
+def test_pack_and_unpack(n, k):
+    rng = np.random.default_rng(n)
+    codes = rng.integers(-8, 8, (n, k)).astype(np.int8)
+    packed = torch.zeros(tb.tb_q4_packed_bytes(n, k), dtype=torch.uint8, device=DEV)
+    count = torch.zeros(1, dtype=torch.int32, device=DEV)
+    tb.tb_q4_pack(torch.from_numpy(codes).to(DEV), n, k, packed, count)
+    assert np.array_equal(packed.cpu().numpy().reshape(n, k // 2), q4o.pack(codes)) and int(count) == 0
+    back = torch.full((n, k), 77, dtype=torch.int8, device=DEV)
+    tb.tb_q4_unpack(packed, n, k, back)
+    assert np.array_equal(back.cpu().numpy(), codes)
+    # values outside the range go to its nearer end and are counted
+    wild = codes.copy()
+    wild[0, [0, 5, 127]] = [8, -9, -128]
+    tb.tb_q4_pack(torch.from_numpy(wild).to(DEV), n, k, packed, count)
+    assert np.array_equal(packed.cpu().numpy().reshape(n, k // 2), q4o.pack(np.clip(wild, -8, 7))) and int(count) == 3
+    tb.tb_q4_pack(torch.from_numpy(wild).to(DEV), n, k, packed)  # no counter
+
+
+@pytest.mark.parametrize("n,k,folded", [(1, 128, True), (9, 1152, True), (301, 2048, True), (7, 640, True), (1, 1024, False),
+                                        (67, 5120, False), (301, 2048, False)])
+@pytest.mark.parametrize("wt", ["bf16", "fp16", "fp32"])
+def test_prepare_bitexact(n, k, folded, wt):
+    rng = np.random.default_rng(n + k)
+    v = rng.standard_normal((n, k)) * 0.02 * np.exp(rng.standard_normal((n, 1)))
+    v = np.round(v * 2.0 ** 22) / 2.0 ** 22  # fp32 values whose folded sums are exact in fp64
+    w = torch.from_numpy(v).to(T[wt][1])
+    w[0, :128] = 0
+    if k >= 1024:
+        w[-1, -1024:] = 0
+    signs = None if folded else draw_signs(rng, k)
+    packed = torch.zeros(n, k // 2, dtype=torch.uint8, device=DEV)
+    scales = torch.zeros(n, k // 128, dtype=torch.float16, device=DEV)
+    tb.tb_q4_prepare_weights(w.to(DEV), T[wt][0], signs.to(DEV) if signs is not None else None, n, k, packed, scales)
+    q, s = q4o.prepare_weights(w.double().numpy(), None if folded else signs.numpy())
+    assert np.array_equal(scales.cpu().numpy().view(np.uint16), s.view(np.uint16))
+    assert np.array_equal(packed.cpu().numpy(), q4o.pack(q))
+
+
+@pytest.mark.parametrize("size", [1e9, 30000.0, 1e-6, 3e-7, 1e-9])
+def test_prepare_ends_of_the_scale(size):
+    rng = np.random.default_rng(2)
+    w = torch.from_numpy(rng.standard_normal((3, 256)) * size).float()
+    packed = torch.zeros(3, 128, dtype=torch.uint8, device=DEV)
+    scales = torch.zeros(3, 2, dtype=torch.float16, device=DEV)
+    tb.tb_q4_prepare_weights(w.to(DEV), tb.TB_FP32, None, 3, 256, packed, scales)
+    q, s = q4o.prepare_weights(w.double().numpy())
+    assert np.array_equal(scales.cpu().numpy(), s) and np.array_equal(packed.cpu().numpy(), q4o.pack(q))
+
+
+@pytest.mark.parametrize("wt", ["bf16", "fp32"])
+def test_prepare_values_on_borders(wt):
+    """Every q + 1/2 of a group whose scale is a power of two, and its
+    neighbours in the input's type: halves go to even."""
+    for scale in (1.0, 2.0 ** -7):
+        v = [7.0]
+        for q in range(-7, 7):
+            b = torch.tensor((q + 0.5) * scale).to(T[wt][1])
+            v += [(q + 0.5), torch.nextafter(b, torch.tensor(float("inf")).to(b)).item() / scale,
+                  torch.nextafter(b, torch.tensor(-float("inf")).to(b)).item() / scale]
+        w = torch.zeros(1, 128)
+        w[0, :len(v)] = torch.tensor(v) * scale
+        w = w.to(T[wt][1])
+        packed = torch.zeros(1, 64, dtype=torch.uint8, device=DEV)
+        scales = torch.zeros(1, 1, dtype=torch.float16, device=DEV)
+        tb.tb_q4_prepare_weights(w.to(DEV), T[wt][0], None, 1, 128, packed, scales)
+        q, s = q4o.prepare_weights(w.double().numpy())
+        assert float(scales) == scale == s[0, 0]
+        assert np.array_equal(packed.cpu().numpy(), q4o.pack(q))
+
+
+# ------------------------------------------------------------------ linear
+@functools.lru_cache(maxsize=8)
+def weights(seed, n, k):
+    rng = np.random.default_rng(seed)
+    codes = rng.integers(-8, 8, (n, k)).astype(np.int8)
+    scales = (np.abs(rng.standard_normal((n, k // 128))) * 0.01).astype(np.float16)
+    scales[0, 0] = 0
+    packed = torch.from_numpy(q4o.pack(codes)).to(DEV)
+    return codes, scales, packed, torch.from_numpy(scales.view(np.int16)).to(DEV)
+
+
+class Linear:
+    def __init__(self, seed, m, n, k, xt="bf16", group=0, signs=False, yt="bf16"):
+        rng = np.random.default_rng(1000 + seed)
+        self.m, self.n, self.k, self.xt, self.group, self.yt = m, n, k, xt, group, yt
+        self.codes, self.scales, self.packed, self.dscales = weights(seed, n, k)
+        x = rng.standard_normal((m, k)) * (0.2 + rng.random((m, 1)))
+        x[rng.random((m, k)) < 0.01] *= 20.0
+        self.xs = None
+        if group:
+            top = 127.0 if xt == "int8" else 448.0
+            xg = x.reshape(m, k // group, group)
+            xs = (np.abs(xg).max(2) / top).astype(np.float32)
+            x = (xg / xs[:, :, None]).reshape(m, k)
+            x = np.clip(np.rint(x), -127, 127) if xt == "int8" else np.clip(x, -448, 448)
+            self.xs = torch.from_numpy(xs)
+        self.x = torch.from_numpy(x).float().to(T[xt][1])
+        self.signs = draw_signs(rng, k) if signs else None
+
+    def run(self, guard=0, stream=None):
+        self.dx = self.x.to(DEV)
+        self.dxs = self.xs.to(DEV) if self.xs is not None else None
+        self.ds = self.signs.to(DEV) if self.signs is not None else None
+        self.y = torch.full((self.m + guard, self.n), 77.0, device=DEV).to(T[self.yt][1])
+        self.wsb = tb.tb_q4_linear_workspace(self.m, self.n, self.k)
+        self.ws = torch.full((self.wsb + 256,), 0xFF, dtype=torch.uint8, device=DEV)
+        torch.cuda.synchronize()
+        self.call(stream)
+        torch.cuda.synchronize()
+        assert (self.ws[self.wsb:] == 0xFF).all()
+        return self
+
+    def call(self, stream=None):
+        tb.tb_q4_linear(self.dx, T[self.xt][0], self.dxs, self.group, self.packed, self.dscales, self.m, self.n, self.k,
+                        self.ds, self.y, T[self.yt][0], self.ws, self.wsb, stream=stream)
+
+    def check(self):
+        xs = self.xs.numpy() if self.xs is not None else None
+        sg = self.signs.numpy() if self.signs is not None else None
+        x = self.x.to(torch.float64).numpy()
+        ref = q4o.linear(x, self.codes, self.scales, xs, sg)
+        xr = q4o.orc.rotate(x, sg) if sg is not None else x
+        big = q4o.linear(np.abs(xr), np.abs(self.codes), self.scales, xs)
+        y = self.y[:self.m].cpu().double().numpy()
+        fi = torch.finfo(T[self.yt][1])
+        half = np.abs(ref) * fi.eps / 2 + fi.smallest_normal * fi.eps
+        exact = self.m <= 16 and sg is None
+        assert (np.abs(y - ref) <= big * (2.0 ** -17 if exact else 2.0 ** -10) + half).all()
+        if not exact:
+            rel = np.linalg.norm(y - ref) / np.linalg.norm(ref)
+            assert rel <= 2.0 ** -11 + fi.eps / 2, rel
+        return self
+
+
+SHAPES = [(1, 1, 128), (1, 7, 256), (1, 1000, 640), (1, 2049, 5120), (2, 64, 384), (3, 129, 1152), (5, 18, 17408),
+          (7, 333, 2048), (8, 1000, 1024), (9, 257, 1920), (15, 40, 128), (16, 1001, 1280), (17, 255, 384), (24, 100, 512),
+          (31, 129, 2048), (32, 512, 1152), (33, 1001, 1920), (47, 30, 640), (64, 300, 1024), (65, 31, 128), (100, 1, 256),
+          (128, 400, 896), (129, 257, 640), (200, 513, 1024), (300, 77, 2176), (513, 600, 256)]
+KINDS = [("bf16", 0), ("fp16", 0), ("int8", 1), ("int8", 128), ("e4m3", 1), ("e4m3", 128)]
+
+
+@pytest.mark.parametrize("m,n,k", SHAPES)
+@pytest.mark.parametrize("xt,group", KINDS)
+def test_linear(m, n, k, xt, group):
+    yt = {"bf16": "bf16", "fp16": "fp16", "int8": "fp32", "e4m3": "bf16"}[xt]
+    Linear(n, m, n, k, xt, k if group == 1 else group, False, yt).run().check()
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 513, 1024), (1, 100, 5120), (4, 77, 2048), (16, 300, 5120), (31, 64, 1024),
+                                   (65, 200, 2048), (300, 300, 1024)])
+@pytest.mark.parametrize("xt,yt", [("bf16", "fp32"), ("fp16", "fp16")])
+def test_linear_rotated(m, n, k, xt, yt):
+    Linear(n, m, n, k, xt, 0, True, yt).run().check()
+
+
+@pytest.mark.parametrize("m", [1, 6, 16, 40, 130])
+@pytest.mark.parametrize("yt", ["bf16", "fp16", "fp32"])
+def test_output_types_and_rows_behind_the_last(m, yt):
+    c = Linear(300, m, 300, 512, "bf16", 0, False, yt).run(guard=3).check()
+    assert (c.y[m:].float() == 77.0).all()
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 17408, 5120), (1, 1024, 5120), (4, 5120, 17408), (16, 6144, 5120), (2, 40000, 1024),
+                                   (16, 5120, 17408), (20, 4096, 2048)])
+def test_linear_full_shapes(m, n, k):
+    rng = np.random.default_rng(n)
+    packed = torch.randint(0, 256, (n, k // 2), dtype=torch.uint8, device=DEV)
+    scales = (torch.randn(n, k // 128, device=DEV).abs() * 0.01).to(torch.float16)
+    x = torch.from_numpy(rng.standard_normal((m, k))).to(torch.bfloat16).to(DEV)
+    y = torch.full((m, n), float("nan"), device=DEV)
+    wsb = tb.tb_q4_linear_workspace(m, n, k)
+    ws = torch.empty(wsb, dtype=torch.uint8, device=DEV)
+    tb.tb_q4_linear(x, tb.TB_BF16, None, 0, packed, scales, m, n, k, None, y, tb.TB_FP32, ws, wsb)
+    w = torch.stack((packed & 15, packed >> 4), -1).view(n, k).double() - 8.0
+    w *= scales.double().repeat_interleave(128, 1)
+    ref, big = x.double() @ w.T, x.double().abs() @ w.abs().T
+    assert ((y.double() - ref).abs() <= big * (2.0 ** -17 if m <= 16 else 2.0 ** -10)).all()
+    again = torch.empty_like(y)
+    tb.tb_q4_linear(x, tb.TB_BF16, None, 0, packed, scales, m, n, k, None, again, tb.TB_FP32, ws, wsb)
+    assert torch.equal(y, again)
+
+
+def test_weights_past_32_bits():
+    """Packed codes of more than 4 GiB: the rows at the end match a call on them alone."""
+    n, k = 300000, 32768
+    packed = torch.randint(0, 256, (n, k // 2), dtype=torch.uint8, device=DEV)
+    scales = (torch.randn(n, k // 128, device=DEV).abs() * 0.01).to(torch.float16)
+    for m in (1, 40):
+        x = torch.randn(m, k, device=DEV).to(torch.bfloat16)
+        y, part = torch.empty(m, n, device=DEV), torch.empty(m, 64, device=DEV)
+        wsb = tb.tb_q4_linear_workspace(m, n, k)
+        ws = torch.empty(wsb, dtype=torch.uint8, device=DEV)
+        tb.tb_q4_linear(x, tb.TB_BF16, None, 0, packed, scales, m, n, k, None, y, tb.TB_FP32, ws, wsb)
+        tb.tb_q4_linear(x, tb.TB_BF16, None, 0, packed[-64:], scales[-64:], m, 64, k, None, part, tb.TB_FP32, ws, wsb)
+        w = torch.stack((packed[-64:] & 15, packed[-64:] >> 4), -1).view(64, k).double() - 8.0
+        w *= scales[-64:].double().repeat_interleave(128, 1)
+        ref, big = x.double() @ w.T, x.double().abs() @ w.abs().T
+        for got in (y[:, -64:], part):
+            assert ((got.double() - ref).abs() <= big * (2.0 ** -17 if m <= 16 else 2.0 ** -10)).all()
+
+
+@pytest.mark.parametrize("m", [1, 8, 16, 48, 200])
+@pytest.mark.parametrize("xt", ["bf16", "fp16"])
+def test_no_numbers_stay_in_their_row(m, xt):
+    c = Linear(90, m, 90, 640, xt, 0, False, "fp32")
+    clean = c.run().y.clone()
+    c.x[m // 2, 600] = float("nan")
+    bad = c.run().y.clone()
+    assert torch.isnan(bad[m // 2]).all()
+    keep = [i for i in range(m) if i != m // 2]
+    assert torch.equal(bad[keep], clean[keep])
+    c.x[m // 2, 600] = float("inf")
+    c.run()
+    assert not torch.isfinite(c.y[m // 2]).any() and torch.equal(c.y[keep], clean[keep])
+
+
+@pytest.mark.parametrize("m", [1, 16, 40, 150])
+@pytest.mark.parametrize("signs", [False, True])
+@pytest.mark.parametrize("size", [1e30, 1e-30])
+def test_sizes_beyond_fp16(m, signs, size):
+    """bf16 activations far outside fp16's range, some rows of ordinary size, one of zeros."""
+    c = Linear(80, m, 80, 1024, "bf16", 0, signs, "fp32")
+    c.x[::2] *= size
+    if m > 3:
+        c.x[3] = 0.0
+    c.run().check()
+    if m > 3:
+        assert not c.y[3].any()
+
+
+def test_streams_graphs_and_two_at_once():
+    """The same bits on another stream, in a replayed graph, and from two calls
+    in flight at once with a workspace each."""
+    for m, xt, signs in ((1, "bf16", False), (16, "fp16", True), (80, "bf16", False)):
+        a, b = (Linear(s, m, 700, 2048, xt, 0, signs, "bf16").run().check() for s in (700, 701))
+        want = a.y.clone(), b.y.clone()
+        s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+        a.y.zero_(), b.y.zero_()
+        torch.cuda.synchronize()
+        for _ in range(5):
+            a.call(stream=s1)
+            b.call(stream=s2)
+        torch.cuda.synchronize()
+        assert torch.equal(a.y, want[0]) and torch.equal(b.y, want[1])
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            a.call()
+            b.call()
+            a.call()
+        a.y.zero_(), b.y.zero_()
+        for _ in range(2):
+            g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a.y, want[0]) and torch.equal(b.y, want[1])
+
+
+# ------------------------------------------------------------------ as they are used together
+@pytest.mark.parametrize("m", [1, 5, 16, 33, 140])
+@pytest.mark.parametrize("yt,group", [("int8", 128), ("e4m3", 0), ("bf16", None)])
+def test_norm_then_linear(m, yt, group):
+    """prepare -> (norm with residual and rotation -> 8 bits) -> linear, in one
+    stream without a wait between them, twice; against the float64 chain on the
+    values the norm stored."""
+    n, k = 600, 2048
+    rng = np.random.default_rng(m)
+    dense = torch.from_numpy(rng.standard_normal((n, k)) * 0.02).to(torch.bfloat16).to(DEV)
+    signs = draw_signs(rng, k).to(DEV)
+    packed = torch.empty(n, k // 2, dtype=torch.uint8, device=DEV)
+    scales = torch.empty(n, k // 128, dtype=torch.float16, device=DEV)
+    tb.tb_q4_prepare_weights(dense, tb.TB_BF16, signs, n, k, packed, scales)
+    x, r = (torch.from_numpy(rng.standard_normal((m, k))).to(torch.bfloat16).to(DEV) for _ in range(2))
+    w = torch.ones(k, dtype=torch.bfloat16, device=DEV)
+    group = k if group == 0 else group
+    a = torch.empty(m, k, dtype=T[yt][1], device=DEV)
+    xs = torch.empty(m, k // group, device=DEV) if group else None
+    h, y = torch.empty_like(r), torch.empty(m, n, device=DEV)
+    wsb = tb.tb_q4_linear_workspace(m, n, k)
+    ws = torch.empty(wsb, dtype=torch.uint8, device=DEV)
+    for _ in range(2):
+        tb.tb_rms_norm(x, tb.TB_BF16, r, h, tb.TB_BF16, w, tb.TB_BF16, 1e-6, signs, m, k, a, T[yt][0], xs, group or 0)
+        tb.tb_q4_linear(a, T[yt][0], xs, group or 0, packed, scales, m, n, k, None, y, tb.TB_FP32, ws, wsb)
+    torch.cuda.synchronize()
+    q, s = q4o.prepare_weights(dense.double().cpu().numpy(), signs.cpu().numpy())
+    assert np.array_equal(packed.cpu().numpy(), q4o.pack(q))
+    av = a.to(torch.float64).cpu().numpy()
+    ref = q4o.linear(av, q, s, xs.cpu().numpy() if group else None)
+    got = y.cpu().double().numpy()
+    assert np.linalg.norm(got - ref) <= 2.0 ** -11 * np.linalg.norm(ref)
+    # and it is near the dense layer on the norm: 8-bit and 4-bit steps, uniform
+    # errors of step / sqrt(12): weights max/7 with max about 2.8 sigma in 128
+    # values, 0.12 of sigma; e4m3 2^-4 / sqrt(3) = 0.04; together under 0.15
+    norm = q4o.rms_norm((x.float() + r.float()).to(torch.bfloat16).double().cpu().numpy(), None, 1e-6)
+    dref = norm @ dense.double().cpu().numpy().T
+    assert np.linalg.norm(got - dref) <= 0.15 * np.linalg.norm(dref)
+
+
+@pytest.mark.parametrize("m", [1, 40])
+def test_norm_then_ternary_linear(m):
+    """The norm with the rotation in front of the ternary layer (signs NULL there)
+    gives what the layer gives for the unrotated norm with its signs."""
+    n, k = 512, 2048
+    rng = np.random.default_rng(50 + m)
+    codes = torch.from_numpy(rng.integers(-1, 2, (n, k)).astype(np.int8)).to(DEV)
+    packed = torch.empty(tb.tb_packed_bytes("2bit", n, k), dtype=torch.uint8, device=DEV)
+    tb.tb_pack_ternary("2bit", codes, n, k, packed)
+    scales = (torch.from_numpy(np.abs(rng.standard_normal((n, k // 128))) * 0.02).to(torch.float16)).to(DEV)
+    signs = draw_signs(rng, k).to(DEV)
+    x = torch.from_numpy(rng.standard_normal((m, k))).to(torch.bfloat16).to(DEV)
+    plain, rot = torch.empty(m, k, device=DEV), torch.empty(m, k, device=DEV)
+    args = (None, None, 0, None, 0, 1e-6)
+    tb.tb_rms_norm(x, tb.TB_BF16, *args, None, m, k, plain, tb.TB_FP32)
+    tb.tb_rms_norm(x, tb.TB_BF16, *args, signs, m, k, rot, tb.TB_FP32)
+    wsb = tb.tb_ternary_linear_workspace("2bit", m, n, k)
+    ws = torch.empty(wsb, dtype=torch.uint8, device=DEV)
+    y = [torch.empty(m, n, device=DEV) for _ in range(2)]
+    tb.tb_ternary_linear(plain, tb.TB_FP32, packed, scales, "2bit", m, n, k, signs, y[0], tb.TB_FP32, ws, wsb)
+    tb.tb_ternary_linear(rot, tb.TB_FP32, packed, scales, "2bit", m, n, k, None, y[1], tb.TB_FP32, ws, wsb)
+    # both are within 2e-3 of the exact product in relative L2
+    assert float((y[0] - y[1]).norm() / y[0].norm()) <= 4e-3
