@@ -1,10 +1,11 @@
-// Prefill GEMM on a pair of CTAs (tcgen05 cta_group::2), 2-bit slot format
-// and 1-bit g128, with the unpacked weights in tensor memory.
+// Prefill GEMM on a pair of CTAs (tcgen05 cta_group::2), 2-bit slot format,
+// 1-bit g128 and 4-bit g128, with the unpacked weights in tensor memory.
 //
 // y[m, n] = sum_k x'[m, k] * w[n, k],  w = s[n, k/128] * t[n, k]  (ternary
 // g128: news.ditty.ir, second paragraph).  The weights are the MMA's M side:
 // each thread unpacks its weight row into exact fp16 s*t (t is -1, 0 or +1 and
-// s an fp16 value) and writes it straight into tensor memory with tcgen05.st,
+// s an fp16 value; 4-bit weights: q in -8..7, s*q rounded to fp16, 2^-11
+// relative) and writes it straight into tensor memory with tcgen05.st,
 // where the MMA reads it as operand A.  The tokens are the N side: x' tiles
 // come by TMA into shared memory as operand B.  So shared memory carries only
 // the x' tiles and the packed codes; the fp16 weights never touch it.
@@ -46,7 +47,10 @@
 //            unpack warps read D out.
 // The code order inside a 16-code chunk is the one the prep kernel writes x'
 // in (k = 0, 8, 1, 9, ..., 7, 15): the TMEM column j of a chunk holds the fp16
-// pair (w_j, w_{j+8}).
+// pair (w_j, w_{j+8}).  4-bit codes: the order inside 8 codes is k = 0, 4, 1,
+// 5, 2, 6, 3, 7, which masks and one shift of a packed word deliver, and x'
+// carries a scale per token (a power of two that keeps its row inside fp16,
+// times the scale of an 8-bit row), applied when D is read out.
 //
 // Every wait is bounded; after a timeout a role stops waiting, records a fault
 // word and still reaches the final cluster barrier, so no CTA leaves while its
@@ -94,7 +98,25 @@ struct GemmParams {
   int M, N, K;
   void* y;
   const uint16_t* scales;  // [N, K/128] fp16 bits
+  const float* xscale;     // 4-bit weights: factor of each token, padded to whole token tiles
 };
+
+// 8 codes c = q + 8 of a 4-bit word as four half2 (q_j, q_{j+4}) s, rounded
+// once: 1024 + c (or 1024 + 16 c, from the higher nibble of a byte) is an exact
+// fp16 bit pattern, and taking the bias off is exact as well.
+__device__ __forceinline__ void gp_unpack_q4(uint32_t w, __half2 s2, uint32_t* o) {
+  const __half2 kbias = __float2half2_rn(-1032.f), k16 = __float2half2_rn(0.0625f), km72 = __float2half2_rn(-72.f);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t ws = h ? w >> 8 : w;
+    const uint32_t lo = (ws & 0x000F000Fu) | 0x64006400u, hi = (ws & 0x00F000F0u) | 0x64006400u;
+    const __half2 qlo = __hadd2(*reinterpret_cast<const __half2*>(&lo), kbias);
+    const __half2 qhi = __hfma2(*reinterpret_cast<const __half2*>(&hi), k16, km72);
+    const __half2 vlo = __hmul2(qlo, s2), vhi = __hmul2(qhi, s2);
+    o[2 * h] = *reinterpret_cast<const uint32_t*>(&vlo);
+    o[2 * h + 1] = *reinterpret_cast<const uint32_t*>(&vhi);
+  }
+}
 
 // 16 codes of a 2-bit word (code u in bits 2u) as 16 bytes c_u = t_u + 1 in
 // natural order: the masks m_j = (w >> 2j) & 0x03030303 hold c_{4b+j} in byte
@@ -135,9 +157,10 @@ static_assert(kGpDCols + kGpASlots * kGpACols <= kGpTmemCols, "TMEM budget");
 
 // x half tile of a stage: two atoms of BT/2 rows x 128 bytes
 __host__ __device__ constexpr int gp_x_bytes(int bt) { return bt / 2 * 2 * kGpAtomBytes; }
-// codes of a stage per row: 2 bits (fmt 0) or 1 bit (fmt 2) a code
+// codes of a stage per row: 2 bits (fmt 0), 1 bit (fmt 2) or 4 bits (fmt 3) a code
+constexpr int kGpQ4 = 3;
 __host__ __device__ constexpr int gp_w_row_bytes(int fmt, bool integer) {
-  return fmt == 0 ? gp_bk(integer) / 4 : gp_bk(integer) / 8;
+  return fmt == 0 ? gp_bk(integer) / 4 : (fmt == kGpQ4 ? gp_bk(integer) / 2 : gp_bk(integer) / 8);
 }
 __host__ __device__ constexpr int gp_stage_bytes(int bt, int fmt, bool integer) {
   return gp_x_bytes(bt) + kGpRows * gp_w_row_bytes(fmt, integer);
@@ -230,14 +253,14 @@ struct GemmPairTiles {
   int tiles_n, tiles_m;
 };
 
-// kFmt: 0 = 2-bit slots, 2 = 1-bit g128.  kInt: integer mode (int8 x, no
+// kFmt: 0 = 2-bit slots, 2 = 1-bit g128, 3 = 4-bit g128.  kInt: integer mode (int8 x, no
 // rotation, no scales, exact int32 y; A = t as signed bytes), else fp16 x' and
 // A = fp16(s t).
 template <int BT, typename TOut, int kFmt, bool kInt>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGpThreads, 1)
     gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                      const GemmParams p, const GemmPairTiles tl) {
-  static_assert(kFmt == 0 || kFmt == 2, "2-bit or 1-bit codes");
+  static_assert(kFmt == 0 || kFmt == 2 || (kFmt == kGpQ4 && !kInt), "2-bit, 1-bit or 4-bit codes");
   static_assert(BT % 64 == 0 && BT >= 128 && BT <= kGpDCols, "token tile");
   constexpr int kBK = gp_bk(kInt), kAtomK = gp_atom_k(kInt), kWr = gp_w_row_bytes(kFmt, kInt);
   constexpr int kX = gp_x_bytes(BT), kAtom = kX / 2, kW = kGpRows * kWr;
@@ -375,6 +398,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGpThreads, 1)
         return;
       }
       tc_fence_after();
+      if constexpr (kFmt == kGpQ4) pdl_wait();  // the tokens' factors come from the prep kernel
       // 16-bit outputs are converted as they come (pairs of tokens in one
       // register), so the warp holds half as many registers until D is free
       constexpr bool kPack = sizeof(TOut) == 2;
@@ -384,9 +408,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGpThreads, 1)
         uint32_t v[32];
         tmem_ld_cols<32>(tmem_d + lane_addr + static_cast<uint32_t>(set * kCols + c), v);
         tmem_ld_wait();
+        if constexpr (kFmt == kGpQ4) {
+          const float4* xs = reinterpret_cast<const float4*>(p.xscale + tile_m0(done) + set * kCols + c);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float4 f = __ldcg(xs + j);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              v[4 * j + e] = __float_as_uint(__uint_as_float(v[4 * j + e]) * (&f.x)[e]);
+          }
+        }
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {
-          if constexpr (kPack) {
+          if constexpr (sizeof(TOut) == 2 && __is_same(TOut, __half)) {
+            const __half2 h2 = __floats2half2_rn(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+            h[(c + j) / 2] = *reinterpret_cast<const uint32_t*>(&h2);
+          } else if constexpr (kPack) {
             const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
             h[(c + j) / 2] = *reinterpret_cast<const uint32_t*>(&b2);
           } else {
@@ -430,8 +467,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGpThreads, 1)
       }
       const uint8_t* wrow = smem + s * kStage + kX + r * kWr;
       uint4 wv[kWr / 16];
+      // 4-bit rows of 64 bytes come 64B-swizzled (16-byte chunk u at u ^ (r / 2) % 4): no bank conflict
 #pragma unroll
-      for (int u = 0; u < kWr / 16; ++u) wv[u] = *reinterpret_cast<const uint4*>(wrow + 16 * u);
+      for (int u = 0; u < kWr / 16; ++u)
+        wv[u] = *reinterpret_cast<const uint4*>(wrow + 16 * (kFmt == kGpQ4 ? u ^ ((r >> 1) & 3) : u));
       __syncwarp();
       if (lane == 0) mbar_arrive(&sfree[s]);  // the codes are in registers
       // the MMAs of stage g - 4 are done with this A slot
@@ -465,6 +504,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGpThreads, 1)
 #pragma unroll
             for (int rr = 0; rr < 8; ++rr) o[8 * u + rr] = ((gi8_bits4(w, rr) << 1) + 0x7F7F7F7Fu) ^ 0x80808080u;
           }
+        } else if constexpr (kFmt == kGpQ4) {
+#pragma unroll
+          for (int wd = 0; wd < 8; ++wd) gp_unpack_q4((&wv[0].x)[8 * half + wd], s2, o + 4 * wd);
         } else if constexpr (kFmt == 2) {
           // chunk c of the 128 codes (16 codes) is half c & 1 of word c >> 1.
           // z holds the chunk's low 8 codes in bits 0-7 and its high 8 in bits

@@ -61,4 +61,92 @@ __global__ void __launch_bounds__(32 * kQ4Warps)
   }
 }
 
+// ---------------------------------------------------------------------------
+// Activation prep: x (bf16, fp16, or 8 bits with scales), rotated when signs is
+// non-null, as fp16 in the order that a packed word is unpacked in (k = 0, 4, 1,
+// 5, 2, 6, 3, 7 inside 8), with one fp32 factor a token.  The factor is the
+// power of two that brings the row's largest magnitude under 2^15 (rotated: 2^10,
+// a block's sums can grow 32-fold), so that bf16 rows of any size keep their 8
+// bits in fp16; an 8-bit row with one scale is exact as it is and its scale is
+// the factor.  Values below 2^-29 of the row's largest lose bits.
+// One block of 128 threads a row; two passes over it (the second hits L2).
+template <typename TIn>
+__device__ __forceinline__ void q4_load8(const TIn* p, float v[8]) { load8<TIn>(p, v); }
+template <>
+__device__ __forceinline__ void q4_load8<int8_t>(const int8_t* p, float v[8]) { load_signs8(p, v); }
+template <>
+__device__ __forceinline__ void q4_load8<__nv_fp8_e4m3>(const __nv_fp8_e4m3* p, float v[8]) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = i < 2 ? u.x : u.y;
+    const __half2_raw r =
+        __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> (16 * (i & 1))), __NV_E4M3);
+    const float2 f = __half22float2(__half2(r));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+
+template <typename TIn>
+__global__ void __launch_bounds__(kHThreads)
+    q4_prep_kernel(const TIn* __restrict__ x, const float* __restrict__ x_scales, int group,
+                   const int8_t* __restrict__ signs, __half* __restrict__ out, float* __restrict__ factor, int K) {
+  constexpr bool k8 = sizeof(TIn) == 1;
+  __shared__ float sm[kHB];
+  __shared__ uint32_t red[kHThreads / 32];
+  pdl_launch_dependents();
+  const int64_t row = blockIdx.x;
+  const int tid = threadIdx.x, G = K / 128;
+  const TIn* xr = x + row * K;
+  // the largest magnitude of the row as fp32 bits (NaN and infinity above all)
+  float f = 1.f;    // x' = x f
+  float out_f = 1.f;  // x = x' out_f
+  if (!k8 || group == 128) {
+    uint32_t mb = 0;
+    if constexpr (k8) {
+      for (int g = tid; g < G; g += kHThreads) mb = max(mb, abs_bits(x_scales[row * G + g] * 448.f));
+    } else {
+      for (int k = 8 * tid; k < K; k += 8 * kHThreads) {
+        float v[8];
+        q4_load8<TIn>(xr + k, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mb = max(mb, abs_bits(v[i]));
+      }
+    }
+    mb = block_max_bits(mb, red);
+    // 2^e <= largest < 2^(e+1); a row that holds a NaN or an infinity stays as it is
+    const int top = signs != nullptr ? 9 : 14;
+    const int e = mb >= kInfBits ? 0 : max(static_cast<int>(mb >> 23) - 127, -96) - top;
+    f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    out_f = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+  } else {
+    out_f = x_scales[row];
+  }
+  if (tid == 0) factor[row] = out_f;
+  for (int k = 8 * tid; k < K; k += 8 * kHThreads) {
+    float v[8];
+    q4_load8<TIn>(xr + k, v);
+    float c = f;
+    if constexpr (k8) {
+      if (group == 128) c *= x_scales[row * G + (k >> 7)];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= c;
+    if constexpr (!k8) {
+      if (signs != nullptr) {
+        float d[8];
+        load_signs8(signs + k, d);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= d[i];
+        fwht1024(v, sm);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= kHNorm;
+      }
+    }
+    const float o[8] = {v[0], v[4], v[1], v[5], v[2], v[6], v[3], v[7]};
+    store8<__half>(out + row * K + k, o);
+  }
+}
+
 }  // namespace tb

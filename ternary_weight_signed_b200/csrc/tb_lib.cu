@@ -955,6 +955,7 @@ tb_status run_gemm_2bit(const LinearArgs& a, const DevInfo* d) {
   gp.K = static_cast<int>(a.K);
   gp.y = a.y;
   gp.scales = a.scales;
+  gp.xscale = nullptr;
   GemmPairTiles tl;
   tl.tiles_n = static_cast<int>(pairs_n);
   tl.tiles_m = static_cast<int>((a.M + bt - 1) / bt);
@@ -1029,6 +1030,7 @@ tb_status run_gemm_i8(const LinearArgs& a, const DevInfo* d) {
   gp.K = static_cast<int>(a.K);
   gp.y = a.y;
   gp.scales = nullptr;
+  gp.xscale = nullptr;
   GemmPairTiles tl;
   tl.tiles_n = static_cast<int>(pairs_n);
   tl.tiles_m = static_cast<int>((a.M + bt - 1) / bt);
@@ -1120,7 +1122,8 @@ struct Q4Args {
 bool is_8bit_dtype(int t) { return t == TB_INT8 || t == TB_E4M3; }
 
 size_t q4_required_ws(int64_t M, int64_t K) {
-  return (static_cast<size_t>(4) * static_cast<size_t>(M) * static_cast<size_t>(K) + 255) & ~static_cast<size_t>(255);
+  return ((static_cast<size_t>(4) * static_cast<size_t>(M) * static_cast<size_t>(K) + 255) & ~static_cast<size_t>(255)) +
+         static_cast<size_t>((M + 255) / 256) * 1024;
 }
 
 bool q4_sizes_ok(int64_t M, int64_t N, int64_t K) {
@@ -1145,7 +1148,7 @@ tb_status validate_q4(const Q4Args& a) {
   return TB_OK;
 }
 
-tb_status run_q4(const Q4Args& a) {
+tb_status run_q4_simple(const Q4Args& a) {
   float* xf = static_cast<float*>(a.ws);
   if (a.signs != nullptr) {
     const dim3 pg(static_cast<unsigned>(a.M), static_cast<unsigned>(a.K / kHB));
@@ -1164,6 +1167,77 @@ tb_status run_q4(const Q4Args& a) {
       xf, a.packed, a.scales, a.y, a.yt, a.M, a.N, static_cast<int>(a.K));
   return launch_status();
 }
+
+// x' as fp16 [M, K], then the tokens' factors, padded to whole token tiles.
+size_t q4_x_bytes(int64_t M, int64_t K) { return (static_cast<size_t>(M) * K * 2 + 255) & ~static_cast<size_t>(255); }
+
+template <typename TIn>
+void launch_q4_prep(const Q4Args& a, __half* xh, float* factor) {
+  q4_prep_kernel<TIn><<<static_cast<unsigned>(a.M), kHThreads, 0, a.st>>>(
+      static_cast<const TIn*>(a.x), a.x_scales, static_cast<int>(a.x_group), a.signs, xh, factor,
+      static_cast<int>(a.K));
+}
+
+tb_status run_q4_prep(const Q4Args& a, __half* xh, float* factor) {
+  switch (a.xt) {
+    case TB_BF16: launch_q4_prep<__nv_bfloat16>(a, xh, factor); break;
+    case TB_FP16: launch_q4_prep<__half>(a, xh, factor); break;
+    case TB_INT8: launch_q4_prep<int8_t>(a, xh, factor); break;
+    default: launch_q4_prep<__nv_fp8_e4m3>(a, xh, factor); break;
+  }
+  return launch_status();
+}
+
+template <int BT, typename TOut>
+tb_status launch_q4_gemm(const Q4Args& a, const DevInfo* d, const CUtensorMap& tm_x, const CUtensorMap& tm_w,
+                         const GemmParams& gp, const GemmPairTiles& tl) {
+  auto k = gemm_pair_kernel<BT, TOut, kGpQ4, false>;
+  if (allow_smem(k, d) != TB_OK) return TB_ERR_CUDA;
+  // persistent: one cluster per SM pair at most, each walking its tiles
+  const int64_t ntiles = static_cast<int64_t>(tl.tiles_n) * tl.tiles_m;
+  const dim3 grid(static_cast<unsigned>(2 * std::min<int64_t>(ntiles, std::max(1, d->sm_count / 2))));
+  return launch_pdl(k, grid, dim3(kGpThreads), static_cast<size_t>(gp_smem_bytes(BT, kGpQ4, false)), a.st, tm_x, tm_w,
+                    gp, tl);
+}
+
+tb_status run_q4_gemm(const Q4Args& a, const DevInfo* d) {
+  __half* xh = static_cast<__half*>(a.ws);
+  float* factor = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + q4_x_bytes(a.M, a.K));
+  const int bt = a.M <= 128 ? 128 : 256;  // as in run_gemm_2bit
+  CUtensorMap tm_x, tm_w;
+  if (make_map_2d(&tm_x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, xh, a.K, a.M, a.K * 2, gp_atom_k(false),
+                  static_cast<uint32_t>(bt / 2), CU_TENSOR_MAP_SWIZZLE_128B) != TB_OK ||
+      make_map_2d(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, a.packed, a.K / 8, a.N, a.K / 2,
+                  static_cast<uint32_t>(gp_w_row_bytes(kGpQ4, false) / 4), static_cast<uint32_t>(kGpRows),
+                  CU_TENSOR_MAP_SWIZZLE_64B) != TB_OK)
+    return TB_ERR_CUDA;
+  const tb_status st = run_q4_prep(a, xh, factor);
+  if (st != TB_OK) return st;
+  GemmParams gp;
+  gp.M = static_cast<int>(a.M);
+  gp.N = static_cast<int>(a.N);
+  gp.K = static_cast<int>(a.K);
+  gp.y = a.y;
+  gp.scales = a.scales;
+  gp.xscale = factor;
+  GemmPairTiles tl;
+  tl.tiles_n = static_cast<int>((a.N + kGpPairRows - 1) / kGpPairRows);
+  tl.tiles_m = static_cast<int>((a.M + bt - 1) / bt);
+  if (bt == 128) {
+    switch (a.yt) {
+      case TB_FP32: return launch_q4_gemm<128, float>(a, d, tm_x, tm_w, gp, tl);
+      case TB_FP16: return launch_q4_gemm<128, __half>(a, d, tm_x, tm_w, gp, tl);
+      default: return launch_q4_gemm<128, __nv_bfloat16>(a, d, tm_x, tm_w, gp, tl);
+    }
+  }
+  switch (a.yt) {
+    case TB_FP32: return launch_q4_gemm<256, float>(a, d, tm_x, tm_w, gp, tl);
+    case TB_FP16: return launch_q4_gemm<256, __half>(a, d, tm_x, tm_w, gp, tl);
+    default: return launch_q4_gemm<256, __nv_bfloat16>(a, d, tm_x, tm_w, gp, tl);
+  }
+}
+
+tb_status run_q4(const Q4Args& a, const DevInfo* d) { return a.M > 16 ? run_q4_gemm(a, d) : run_q4_simple(a); }
 
 }  // namespace
 
@@ -1509,7 +1583,7 @@ tb_status tb_q4_linear(const void* x, tb_dtype xt, const float* x_scales, int64_
   const DevInfo* d = nullptr;
   st = current_device(&d);
   if (st != TB_OK) return st;
-  return run_q4(a);
+  return run_q4(a, d);
 }
 
 tb_status tb_test_stall_copies(uint32_t stall, uint64_t wait_limit_ns) {
