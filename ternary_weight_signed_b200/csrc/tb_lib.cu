@@ -1121,10 +1121,9 @@ struct Q4Args {
 
 bool is_8bit_dtype(int t) { return t == TB_INT8 || t == TB_E4M3; }
 
-size_t q4_required_ws(int64_t M, int64_t K) {
-  return ((static_cast<size_t>(4) * static_cast<size_t>(M) * static_cast<size_t>(K) + 255) & ~static_cast<size_t>(255)) +
-         static_cast<size_t>((M + 255) / 256) * 1024;
-}
+// x' as fp16 [M, K], then the tokens' factors, padded to whole token tiles.
+size_t q4_x_bytes(int64_t M, int64_t K) { return (static_cast<size_t>(M) * K * 2 + 255) & ~static_cast<size_t>(255); }
+size_t q4_required_ws(int64_t M, int64_t K) { return q4_x_bytes(M, K) + static_cast<size_t>((M + 255) / 256) * 1024; }
 
 bool q4_sizes_ok(int64_t M, int64_t N, int64_t K) {
   return M >= 1 && N >= 1 && K >= 128 && K % 128 == 0 && M <= kMaxDim && N < (int64_t(1) << 30) && K <= kMaxDim &&
@@ -1147,29 +1146,6 @@ tb_status validate_q4(const Q4Args& a) {
   if (!aligned(a.ws, 16)) return TB_ERR_ALIGN;
   return TB_OK;
 }
-
-tb_status run_q4_simple(const Q4Args& a) {
-  float* xf = static_cast<float*>(a.ws);
-  if (a.signs != nullptr) {
-    const dim3 pg(static_cast<unsigned>(a.M), static_cast<unsigned>(a.K / kHB));
-    if (a.xt == TB_BF16)
-      prep_store_kernel<__nv_bfloat16, float><<<pg, kHThreads, 0, a.st>>>(static_cast<const __nv_bfloat16*>(a.x),
-                                                                          a.signs, xf, a.K);
-    else
-      prep_store_kernel<__half, float><<<pg, kHThreads, 0, a.st>>>(static_cast<const __half*>(a.x), a.signs, xf, a.K);
-  } else {
-    const int64_t n = a.M * a.K;
-    q4_convert_kernel<<<static_cast<unsigned>((n + 255) / 256), 256, 0, a.st>>>(
-        a.x, a.xt, a.x_scales, static_cast<int>(a.x_group), xf, n, static_cast<int>(a.K));
-  }
-  if (launch_status() != TB_OK) return TB_ERR_CUDA;
-  q4_linear_kernel<<<static_cast<unsigned>((a.N + kQ4Warps - 1) / kQ4Warps), 32 * kQ4Warps, 0, a.st>>>(
-      xf, a.packed, a.scales, a.y, a.yt, a.M, a.N, static_cast<int>(a.K));
-  return launch_status();
-}
-
-// x' as fp16 [M, K], then the tokens' factors, padded to whole token tiles.
-size_t q4_x_bytes(int64_t M, int64_t K) { return (static_cast<size_t>(M) * K * 2 + 255) & ~static_cast<size_t>(255); }
 
 template <typename TIn>
 void launch_q4_prep(const Q4Args& a, __half* xh, float* factor) {
@@ -1237,7 +1213,133 @@ tb_status run_q4_gemm(const Q4Args& a, const DevInfo* d) {
   }
 }
 
-tb_status run_q4(const Q4Args& a, const DevInfo* d) { return a.M > 16 ? run_q4_gemm(a, d) : run_q4_simple(a); }
+struct Q4DecodePlan {
+  int threads, R, nblocks, Wt, Wk, TPW, S, Gs, clusters;
+  size_t smem;
+};
+
+// Geometry of the decode kernel, by an estimate of the issue slots that the
+// busiest SM spends: a 16-row tile of a 128-group costs about 96 instructions
+// and an MMA per token tile and 16 codes, its activations about 20 per token
+// tile; staging x' costs its bytes.  Two CTAs of 8 warps on an SM, or one of 16.
+// False if x' of a cluster's slice does not fit.
+bool q4_decode_plan(int64_t M64, int64_t N, int64_t K, bool xg, int sm_count, int max_smem, Q4DecodePlan* out) {
+  if (M64 > kQ4DecMaxM) return false;
+  const int M = static_cast<int>(M64), NT = (M + 7) / 8, G = static_cast<int>(K / 128);
+  double best = -1;
+  for (int W = 8; W <= 16; W += 8) {
+    const int cps = W == 8 ? 2 : 1;
+    const int64_t budget = cps == 2 ? (max_smem - 1024) / 2 - 1024 : max_smem;
+    for (int S = 1; S <= 8; S *= 2) {
+      if (S > 1 && G < 2 * S) break;
+      const int Gs = (G + S - 1) / S;
+      const int clusters = std::max(1, sm_count * cps / S);
+      for (int TPW = 1; TPW <= (NT == 1 ? 4 : 2); ++TPW) {
+        if (TPW == 3) continue;
+        const int GP = q4_dec_gp(TPW);
+        for (int Wt = 1; Wt <= W; ++Wt) {
+          const int Wk = W / Wt, rows = 16 * TPW * Wt;
+          const int64_t smem = q4_dec_x_bytes(M, Gs) + q4_dec_xs_bytes(M, Gs, xg) + q4_dec_part_bytes(M, rows, Wk);
+          if (smem > budget) continue;
+          const int64_t rounds = (N + static_cast<int64_t>(rows) * clusters - 1) / (static_cast<int64_t>(rows) * clusters);
+          const int64_t R = (N + clusters * rounds - 1) / (clusters * rounds);
+          const double step = GP * (TPW * (96.0 + 8 * NT) + 20.0 * NT);
+          const int64_t steps = (Gs + Wk * GP - 1) / (Wk * GP);
+          const double issue = cps * W / 4.0 * (rounds * steps * step) * (Wt * Wk) / W;
+          const double sums = cps * static_cast<double>(rounds) * R * M * Wk / 16.0 * (S > 1 ? 2 : 1);
+          const double stage = cps * static_cast<double>(M) * Gs * 256 / 32.0;
+          const double cost = issue + sums + stage + (S > 1 ? 1500.0 * rounds : 0.0);
+          if (best < 0 || cost < best) {
+            best = cost;
+            *out = Q4DecodePlan{32 * W, static_cast<int>(R), static_cast<int>((N + R - 1) / R), Wt, Wk, TPW, S, Gs,
+                                clusters, static_cast<size_t>(smem)};
+          }
+        }
+      }
+    }
+  }
+  return best >= 0;
+}
+
+template <int NT, int TPW, typename TX, bool XG>
+tb_status launch_q4_decode(const Q4DecodeParams& p, const Q4DecodePlan& pl, const DevInfo* d, cudaStream_t st) {
+  auto k = q4_decode_kernel<NT, TPW, TX, XG>;
+  if (allow_smem(k, d) != TB_OK) return TB_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(pl.S * std::min(pl.clusters, pl.nblocks)));
+  cfg.blockDim = dim3(static_cast<unsigned>(pl.threads));
+  cfg.dynamicSmemBytes = pl.smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(pl.S);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pl.S > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, k, p) != cudaSuccess) {
+    cudaGetLastError();
+    return TB_ERR_CUDA;
+  }
+  return TB_OK;
+}
+
+template <int NT, typename TX, bool XG>
+tb_status launch_q4_decode_tiles(const Q4DecodeParams& p, const Q4DecodePlan& pl, const DevInfo* d, cudaStream_t st) {
+  if constexpr (NT == 1) {
+    if (pl.TPW == 4) return launch_q4_decode<NT, 4, TX, XG>(p, pl, d, st);
+  }
+  return pl.TPW == 2 ? launch_q4_decode<NT, 2, TX, XG>(p, pl, d, st) : launch_q4_decode<NT, 1, TX, XG>(p, pl, d, st);
+}
+
+tb_status run_q4_decode(const Q4Args& a, const DevInfo* d, const Q4DecodePlan& pl) {
+  Q4DecodeParams p;
+  p.x = a.x;
+  p.xmode = a.xt == TB_BF16 ? Q4X_BF16 : (a.xt == TB_FP16 ? Q4X_FP16 : (a.xt == TB_INT8 ? Q4X_INT8 : Q4X_E4M3));
+  const bool xg = is_8bit_dtype(a.xt) && a.x_group == 128;
+  p.group_scales = xg ? a.x_scales : nullptr;
+  p.factor = xg ? nullptr : a.x_scales;
+  if (a.signs != nullptr) {
+    __half* xh = static_cast<__half*>(a.ws);
+    float* factor = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + q4_x_bytes(a.M, a.K));
+    const tb_status st = run_q4_prep(a, xh, factor);
+    if (st != TB_OK) return st;
+    p.x = xh;
+    p.xmode = Q4X_PREP;
+    p.factor = factor;
+  }
+  p.packed = a.packed;
+  p.scales = a.scales;
+  p.y = a.y;
+  p.yt = a.yt;
+  p.M = static_cast<int>(a.M);
+  p.N = a.N;
+  p.K = static_cast<int>(a.K);
+  p.R = pl.R;
+  p.nblocks = pl.nblocks;
+  p.Wt = pl.Wt;
+  p.Wk = pl.Wk;
+  p.S = pl.S;
+  p.Gs = pl.Gs;
+  const bool h = p.xmode != Q4X_BF16 && p.xmode != Q4X_INT8;  // int8 codes are exact in bf16, e4m3 ones in fp16
+  if (a.M <= 8) {
+    if (h) return xg ? launch_q4_decode_tiles<1, __half, true>(p, pl, d, a.st) : launch_q4_decode_tiles<1, __half, false>(p, pl, d, a.st);
+    return xg ? launch_q4_decode_tiles<1, __nv_bfloat16, true>(p, pl, d, a.st)
+              : launch_q4_decode_tiles<1, __nv_bfloat16, false>(p, pl, d, a.st);
+  }
+  if (h) return xg ? launch_q4_decode_tiles<2, __half, true>(p, pl, d, a.st) : launch_q4_decode_tiles<2, __half, false>(p, pl, d, a.st);
+  return xg ? launch_q4_decode_tiles<2, __nv_bfloat16, true>(p, pl, d, a.st)
+            : launch_q4_decode_tiles<2, __nv_bfloat16, false>(p, pl, d, a.st);
+}
+
+tb_status run_q4(const Q4Args& a, const DevInfo* d) {
+  Q4DecodePlan pl;
+  const bool xg = is_8bit_dtype(a.xt) && a.x_group == 128;
+  if (q4_decode_plan(a.M, a.N, a.K, xg, d->sm_count, d->max_smem_optin, &pl)) return run_q4_decode(a, d, pl);
+  return run_q4_gemm(a, d);
+}
 
 }  // namespace
 
