@@ -100,87 +100,157 @@ __global__ void __launch_bounds__(kHThreads)
 
 // ---------------------------------------------------------------------------
 // Decode: up to 16 tokens.  The weights are read once and everything else has
-// to fit beside that stream, so the kernel is built around it:
-//   * a lane reads 16 bytes = 32 codes of a row, four lanes a row's 128-group,
-//     straight into registers, one step ahead of the arithmetic; the codes are
-//     never staged (nothing else of the CTA reads them);
-//   * the products run on mma.sync m16n8k16 with the weights as the 16 rows and
-//     the tokens as the 8 columns: q is exact in bf16 and in fp16, the products
-//     are exact in fp32 and a group is summed in the fp32 accumulators (8 MMAs),
-//     then scaled by s once.  A mask and a shift unpack two codes (k, k + 4) of
-//     a packed word at a time, and x' is laid out in shared memory in that order,
-//     one 16-byte load a lane for two MMAs.  The tensor pipe is not what binds
-//     here; staging the unpacked codes for tcgen05 would move them twice more.
-//   * rows are spread over the CTAs, the groups of K over Wk of a CTA's warps
-//     (fp32 partial sums joined in shared memory in a fixed order) and, when x'
-//     of all tokens does not fit one CTA, over the S CTAs of a cluster, which
-//     read each other's partial sums through distributed shared memory.
-// No atomics: the bits do not depend on scheduling.
-constexpr int kQ4DecMaxThreads = 512;
+// to fit beside that stream.
+//   * The products run on mma.sync m16n8k32 in 8-bit integers, 16 weight rows by 8
+//     columns, exact: the codes c = q + 8 as they are (a mask and a shift, 3
+//     instructions for 8 codes), x' as 8-bit planes of a fixed-point number, a
+//     column per plane and token.  Every group has its own power of two: three
+//     planes hold a value to 2^-23 of its group's largest, two to 2^-15, and an int8
+//     is one.  The sums of a group start from -8 sum x, which takes the bias off,
+//     plus the bits of 1.5 2^23, which makes the integer sum a float's mantissa: one
+//     subtraction instead of a conversion.  The groups are added in fp32.
+//   * Measured on B200, cycles an MMA on one of the SM's four tensor pipes:
+//     m16n8k16 f16 15.4, m16n8k32 s8 15.8, m16n8k32 e4m3 35 (no pipe of its own).
+//     tcgen05.mma with 128 rows takes 47-56 cycles an SM for any N up to 64, K = 16:
+//     36 weights a cycle against 128 / (columns / 8) here.
+//   * Each warp streams its own rows: boxes of up to 32 rows x 128 bytes (256
+//     codes) by TMA into a ring of its own, refilled by the warp itself, so no warp
+//     waits for another inside the loop.  K is spread over Wk of a CTA's warps
+//     (fp32 partial sums joined in shared memory in a fixed order) and, when x' does
+//     not fit one CTA, over the S CTAs of a cluster, which read each other's partial
+//     sums through distributed shared memory.  No atomics: the bits do not depend on
+//     scheduling.
+constexpr int kQ4DecWarps = 8;
 constexpr int kQ4DecMaxM = 16;
+constexpr int kQ4DecSlots = 4;       // boxes in flight a warp, at most
+constexpr int kQ4DecInCta = 4;       // tokens whose planes every CTA makes itself
 
-enum : int { Q4X_BF16 = 0, Q4X_FP16 = 1, Q4X_INT8 = 2, Q4X_E4M3 = 3, Q4X_PREP = 4 };
+constexpr int kQ4MagicBits = 0x4B400000;   // 1.5 2^23; adding an integer below 2^22 to the bits adds it to the value
+constexpr float kQ4Magic = 12582912.f;
+
+enum : int { Q4X_BF16 = 0, Q4X_FP16 = 1, Q4X_INT8 = 2, Q4X_E4M3 = 3, Q4X_IMAGE = 4 };
+
+// Planes of a value: three where they cost no column tile more than two would.
+__host__ __device__ constexpr int q4_planes(int xmode, int M) { return xmode == Q4X_INT8 ? 1 : (M <= 5 ? 3 : 2); }
 
 struct Q4DecodeParams {
   const void* x;
-  const float* group_scales;  // [M, G] of an 8-bit x, or NULL
-  const float* factor;        // [M] or NULL
-  const uint8_t* packed;
+  const float* x_scales;  // of an 8-bit x, or of an image: [G][C], then the sums [G][C]
   const uint16_t* scales;
   void* y;
   int64_t N;
-  int M, K, xmode, yt;
-  int R, nblocks;  // rows of a block, blocks (a cluster takes every nclusters-th)
-  int Wt, Wk;      // row-tile classes x K classes of a CTA's warps
-  int S, Gs;       // cluster size, 128-groups of a CTA's K slice
+  int M, K, xmode, x_group, yt;
+  int P, C;         // planes, columns = planes x tokens
+  int rw, nblocks;  // rows of a warp's box; row blocks of Wt rw rows (a cluster takes every nclusters-th)
+  int Wt, Wk;       // row classes x K classes of a CTA's warps
+  int S, Gs;        // cluster size, 128-groups of a CTA's K slice (even)
+  int slots;        // ring of a warp
+  int part_at;      // byte offset of the partial sums in shared memory
 };
 
-__host__ __device__ constexpr int q4_dec_gp(int tpw) { return tpw >= 3 ? 1 : 4 / tpw; }
-__host__ __device__ constexpr int64_t q4_dec_x_bytes(int M, int Gs) { return int64_t(256) * M * Gs; }
-__host__ __device__ constexpr int64_t q4_dec_xs_bytes(int M, int Gs, bool xg) {
-  return xg ? int64_t(4) * 8 * ((M + 7) / 8) * Gs : 0;
+__host__ __device__ constexpr int q4_dec_box_bytes(int tpw) { return 16 * tpw * 128; }
+// shared memory: rings | x planes [Gs][2][C][4] x 16 bytes | factors, sums [Gs][8 NT] each | barriers | partial sums
+__host__ __device__ constexpr int64_t q4_dec_ring_bytes(int tpw, int slots) {
+  return int64_t(kQ4DecWarps) * slots * q4_dec_box_bytes(tpw);
 }
-__host__ __device__ constexpr int64_t q4_dec_part_bytes(int M, int rows, int Wk) { return int64_t(4) * Wk * M * rows; }
+__host__ __device__ constexpr int64_t q4_dec_x_bytes(int C, int Gs) { return int64_t(128) * C * Gs; }
+__host__ __device__ constexpr int64_t q4_dec_f_bytes(int C, int Gs) { return int64_t(64) * ((C + 7) / 8) * Gs; }
+__host__ __device__ constexpr int64_t q4_dec_part_bytes(int C, int rows, int Wk) { return int64_t(4) * Wk * C * rows; }
 
-template <typename TX>
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-  if constexpr (__is_same(TX, __half))
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Codes s and s + 4 of a packed word as the pair (q_s, q_{s+4}): the code set
-// into the mantissa of 128 (bf16) or 1024 (fp16), then the bias taken off, both exact.
-template <typename TX, int s>
-__device__ __forceinline__ uint32_t q4_pair(uint32_t w) {
-  if constexpr (__is_same(TX, __half)) {
-    const uint32_t v = ((s < 2 ? w : w >> 8) & ((s & 1) ? 0x00F000F0u : 0x000F000Fu)) | 0x64006400u;
-    const __half2 h = *reinterpret_cast<const __half2*>(&v);
-    const __half2 q = (s & 1) ? __hfma2(h, __float2half2_rn(0.0625f), __float2half2_rn(-72.f))
-                              : __hadd2(h, __float2half2_rn(-1032.f));
-    return *reinterpret_cast<const uint32_t*>(&q);
-  } else {
-    const uint32_t v = ((w >> (4 * s)) & 0x000F000Fu) | 0x43004300u;
-    const __nv_bfloat162 q =
-        __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&v), __float2bfloat162_rn(-136.f));
-    return *reinterpret_cast<const uint32_t*>(&q);
+// Planes, factors and sums of 8 consecutive values v (place q = 4 c + i of a
+// 128-group: codes 32 c + 8 i ..) of one token; the 16 lanes that hold the group
+// call this together (a whole warp at a time; lanes without a group of their own
+// are not live and store nothing).  xs multiplies the group's values.  Column n
+// of the group goes to dst[(i / 2) C 4 + 4 n + c], half i % 2.
+__device__ __forceinline__ void q4_store_planes(float v[8], bool int8, float xs, int q, int P, int M, int m, int C,
+                                                uint4* dst, float* fdst, int* sdst, bool live) {
+  float f = 1.f, inv = 1.f;
+  if (!int8) {
+    uint32_t mb = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) mb = max(mb, abs_bits(v[j]));
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, o));
+    // the largest under 2^top (1.9921 2^(top - 1): the highest plane stays under 128)
+    const int top = 8 * P - 1;
+    const int e = min(max(static_cast<int>((mb + 0x10200u) >> 23) - 127, -100), 128);
+    f = __uint_as_float(static_cast<uint32_t>(127 + top - 1 - e) << 23);
+    inv = mb >= kInfBits ? __uint_as_float(0x7FC00000u) : __uint_as_float(static_cast<uint32_t>(127 - top + 1 + e) << 23);
+  }
+  int x[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = __float2int_rn(v[j] * f);
+  inv *= xs;
+  const int c = q >> 2, i = q & 3;
+  for (int p = P - 1; p >= 0; --p) {
+    uint32_t w[2] = {0u, 0u};  // bytes (0, 2, 4, 6) and (1, 3, 5, 7)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      w[j & 1] |= (static_cast<uint32_t>(x[j]) & 0xFFu) << (8 * (j >> 1));
+      x[j] = (x[j] + 128) >> 8;
+    }
+    int s = __dp4a(static_cast<int>(w[0]), 0x01010101, __dp4a(static_cast<int>(w[1]), 0x01010101, 0));
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const int n = p * M + m;
+    if (live) {
+      reinterpret_cast<uint2*>(dst + (i >> 1) * 4 * C + 4 * n + c)[i & 1] = make_uint2(w[0], w[1]);
+      if (q == 0) {
+        fdst[n] = inv;
+        sdst[n] = kQ4MagicBits - 8 * s;
+      }
+    }
+    inv *= 256.f;
   }
 }
 
-__device__ __forceinline__ uint4 ldg_stream(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+__device__ __forceinline__ void q4_load8_any(const void* x, int64_t at, int xmode, float v[8]) {
+  switch (xmode) {
+    case Q4X_BF16: load8<__nv_bfloat16>(static_cast<const __nv_bfloat16*>(x) + at, v); break;
+    case Q4X_FP16: load8<__half>(static_cast<const __half*>(x) + at, v); break;
+    case Q4X_INT8: q4_load8<int8_t>(static_cast<const int8_t*>(x) + at, v); break;
+    default: q4_load8<__nv_fp8_e4m3>(static_cast<const __nv_fp8_e4m3*>(x) + at, v); break;
+  }
+}
+
+// The planes of all tokens, once for the whole grid of the decode kernel (more
+// than kQ4DecInCta tokens, or a rotated x): image [G][2][C][4] x 16 bytes, then
+// factors and sums, [G][C] each.  grid (ceil(K / 1024), M), 128 threads.
+__global__ void __launch_bounds__(kHThreads)
+    q4_planes_kernel(const void* __restrict__ x, int xmode, const float* __restrict__ x_scales, int group,
+                     const int8_t* __restrict__ signs, uint4* __restrict__ image, float* __restrict__ factors, int M,
+                     int K, int P, int C) {
+  __shared__ float sm[kHB];
+  pdl_launch_dependents();
+  const int tid = threadIdx.x, m = blockIdx.y, G = K / 128;
+  const int k = blockIdx.x * kHB + 8 * tid;
+  const bool in = k < K;  // K % 128 == 0: whole groups of 16 threads
+  float v[8] = {};
+  if (in) q4_load8_any(x, static_cast<int64_t>(m) * K + k, xmode, v);
+  if (signs != nullptr) {
+    float d[8];
+    load_signs8(signs + k, d);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= d[i];
+    fwht1024(v, sm);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= kHNorm;
+  }
+  const int g = in ? k >> 7 : 0;
+  const bool x8 = xmode == Q4X_INT8 || xmode == Q4X_E4M3;
+  const float xs = x8 ? x_scales[group == 128 ? static_cast<int64_t>(m) * G + g : m] : 1.f;
+  q4_store_planes(v, xmode == Q4X_INT8, xs, tid & 15, P, M, m, C, image + static_cast<int64_t>(g) * 8 * C,
+                  factors + static_cast<int64_t>(g) * C,
+                  reinterpret_cast<int*>(factors + static_cast<int64_t>(G + g) * C), in);
+}
+
+// c += a b, a: 16 x 32 unsigned, b: 32 x 8 signed bytes.
+__device__ __forceinline__ void mma_u8s8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
@@ -189,92 +259,85 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   return v;
 }
 
-// 8 consecutive values of x in the order (0, 4), (1, 5), (2, 6), (3, 7).
-__device__ __forceinline__ uint4 q4_x8(const void* x, int64_t at, int xmode) {
-  if (xmode == Q4X_PREP) return __ldcg(reinterpret_cast<const uint4*>(static_cast<const __half*>(x) + at));
-  if (xmode <= Q4X_FP16) {
-    const uint4 v = __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at));
-    return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
-                      __byte_perm(v.y, v.w, 0x7632));
-  }
-  const uint2 u = __ldcg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(x) + at));
-  uint4 o;
-  if (xmode == Q4X_INT8) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(static_cast<float>(static_cast<int8_t>(u.x >> (8 * i))),
-                                                     static_cast<float>(static_cast<int8_t>(u.y >> (8 * i))));
-      (&o.x)[i] = *reinterpret_cast<const uint32_t*>(&b);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t pair = __byte_perm(u.x, u.y, 0x0040u + 0x0011u * i);  // bytes i and i + 4
-      const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(pair & 0xFFFFu), __NV_E4M3);
-      (&o.x)[i] = static_cast<uint32_t>(r.x) | (static_cast<uint32_t>(r.y) << 16);
-    }
-  }
-  return o;
-}
-
-// NT: token tiles of 8; TPW: 16-row tiles of a warp; TX: type of the products;
-// XG: x has a scale per token and group.
-template <int NT, int TPW, typename TX, bool XG>
-__global__ void __launch_bounds__(kQ4DecMaxThreads, 1) q4_decode_kernel(const Q4DecodeParams p) {
-  constexpr int GP = q4_dec_gp(TPW);  // groups a step: about 8 16-byte loads in flight a lane
-  extern __shared__ __align__(16) uint8_t q4_smem[];
-  const int M = p.M, T = blockDim.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+// NT: column tiles of 8; TPW: 16-row tiles of a warp's box.
+template <int NT, int TPW>
+__global__ void __launch_bounds__(32 * kQ4DecWarps, 2)
+    q4_decode_kernel(const __grid_constant__ CUtensorMap tm_w, const Q4DecodeParams p) {
+  constexpr int kBox = q4_dec_box_bytes(TPW);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int M = p.M, C = p.C, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r = lane >> 2, c = lane & 3;
+  const int rho = (r >> 1) + 4 * (r & 1);  // the fragment's row r is row rho of its 8: no bank conflict below
   const int rank = p.S > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int cluster = static_cast<int>(blockIdx.x) / p.S, nclusters = static_cast<int>(gridDim.x) / p.S;
   const int G = p.K >> 7, G0 = rank * p.Gs, Gn = max(0, min(p.Gs, G - G0));
-  const int rows = 16 * TPW * p.Wt;  // of the partial sums' layout
-  uint4* xf = reinterpret_cast<uint4*>(q4_smem);
-  float* xsg = reinterpret_cast<float*>(q4_smem + q4_dec_x_bytes(M, p.Gs));
-  float* part = reinterpret_cast<float*>(q4_smem + q4_dec_x_bytes(M, p.Gs) + q4_dec_xs_bytes(M, p.Gs, XG));
+  uint8_t* ring = smem + warp * p.slots * kBox;
+  uint4* xf = reinterpret_cast<uint4*>(smem + q4_dec_ring_bytes(TPW, p.slots));
+  float* xsg = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(xf) + q4_dec_x_bytes(C, p.Gs));
+  int* xsum = reinterpret_cast<int*>(xsg + p.Gs * 8 * NT);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(xsg) + q4_dec_f_bytes(C, p.Gs)) +
+                   warp * kQ4DecSlots;
+  float* part = reinterpret_cast<float*>(smem + p.part_at);
 
   const int wt = warp % p.Wt, wk = warp / p.Wt;
-  const bool active = wk < p.Wk;
-  const int nstep = active && Gn > wk * GP ? (Gn - wk * GP + p.Wk * GP - 1) / (p.Wk * GP) : 0;
-  const int64_t stride8 = int64_t(4) * p.K;  // bytes of 8 rows
+  const int nbox = (Gn + 1) >> 1;                                    // boxes of two groups in the slice
+  const int nb = wk < p.Wk && nbox > wk ? (nbox - wk + p.Wk - 1) / p.Wk : 0;  // this warp's, per row block
+  const int mine = (p.nblocks - cluster + nclusters - 1) / nclusters;  // row blocks of this cluster
+  const int total = mine * nb;
+  const int R = p.Wt * p.rw;
+  const uint32_t bytes = static_cast<uint32_t>(p.rw) * 128u;
 
-  uint4 w[GP][TPW][2];
-  uint16_t sc[GP][TPW][2];
-  auto load = [&](int blk, int j) {
-    const int64_t row0 = static_cast<int64_t>(blk) * p.R;
-    const int lim = static_cast<int>(min(static_cast<int64_t>(p.R), p.N - row0)) - 16 * TPW * wt - r;  // rows from r on
-    const int64_t row = row0 + 16 * TPW * wt + r;
-    const int g0 = (j * p.Wk + wk) * GP;
-    const uint8_t* src = p.packed + row * (p.K >> 1) + static_cast<int64_t>(G0 + g0) * 64 + 16 * c;
-    const uint16_t* ssrc = p.scales + row * G + G0 + g0;
-#pragma unroll
-    for (int gg = 0; gg < GP; ++gg) {
-#pragma unroll
-      for (int h = 0; h < 2 * TPW; ++h) {
-        const bool ok = 8 * h < lim && g0 + gg < Gn;
-        w[gg][h >> 1][h & 1] = ok ? ldg_stream(src + h * stride8 + 64 * gg) : make_uint4(0, 0, 0, 0);
-        sc[gg][h >> 1][h & 1] = ok ? __ldg(ssrc + static_cast<int64_t>(8 * h) * G + gg) : uint16_t(0);
-      }
+  // the producer's place: block and box index of the next box to fetch
+  int fb = 0, fj = 0, fs = 0;
+  auto fetch = [&]() {
+    const int row = (cluster + fb * nclusters) * R + wt * p.rw;
+    mbar_arrive_expect_tx(&bars[fs], bytes);
+    tma_load_2d(ring + fs * kBox, &tm_w, (G0 + 2 * (wk + p.Wk * fj)) * 64, row, &bars[fs]);
+    if (++fj == nb) {
+      fj = 0;
+      ++fb;
     }
+    if (++fs == p.slots) fs = 0;
   };
-
-  pdl_launch_dependents();
-  if (nstep > 0) load(cluster, 0);  // weights do not wait for the previous kernel
-  pdl_wait();
-  for (int m = 0; m < M; ++m) {
-    const int64_t base = static_cast<int64_t>(m) * p.K + static_cast<int64_t>(G0) * 128;
-    for (int q = tid; q < 16 * Gn; q += T)  // q = 16 g + 4 c + i: codes 32 c + 8 i of group g
-      xf[((q >> 4) * 4 + (q & 3)) * 4 * M + 4 * m + ((q >> 2) & 3)] = q4_x8(p.x, base + 8 * q, p.xmode);
+  if (lane == 0) {
+    for (int s = 0; s < p.slots; ++s) mbar_init(&bars[s], 1);
+    fence_mbar_init();
+    for (int s = 0; s < p.slots && s < total; ++s) fetch();  // weights do not wait for the previous kernel
   }
-  if constexpr (XG) {
-    for (int q = tid; q < 8 * NT * Gn; q += T) {
-      const int g = q / (8 * NT), m = q - 8 * NT * g;
-      xsg[q] = m < M ? __ldcg(p.group_scales + static_cast<int64_t>(m) * G + G0 + g) : 0.f;
+  pdl_launch_dependents();
+  pdl_wait();
+  if (p.xmode == Q4X_IMAGE) {
+    const uint4* src = static_cast<const uint4*>(p.x) + static_cast<int64_t>(G0) * 8 * C;
+    for (int q = tid; q < 8 * C * Gn; q += 32 * kQ4DecWarps) xf[q] = __ldcg(src + q);
+    for (int q = tid; q < C * Gn; q += 32 * kQ4DecWarps) {
+      const int g = q / C, n = q - g * C;
+      xsg[g * 8 * NT + n] = __ldcg(p.x_scales + static_cast<int64_t>(G0) * C + q);
+      xsum[g * 8 * NT + n] = __ldcg(reinterpret_cast<const int*>(p.x_scales) + static_cast<int64_t>(G + G0) * C + q);
+    }
+  } else {
+    // half a warp makes the planes of one token's group
+    const bool x8 = p.xmode == Q4X_INT8 || p.xmode == Q4X_E4M3;
+    const int items = M * Gn;
+    for (int q0 = 2 * warp; q0 < items; q0 += 2 * kQ4DecWarps) {
+      const bool live = q0 + (lane >> 4) < items;
+      const int q = live ? q0 + (lane >> 4) : q0;
+      const int m = q / Gn, g = q - m * Gn;
+      float v[8];
+      q4_load8_any(p.x, static_cast<int64_t>(m) * p.K + static_cast<int64_t>(G0 + g) * 128 + 8 * (lane & 15), p.xmode, v);
+      const float xs = x8 ? p.x_scales[p.x_group == 128 ? static_cast<int64_t>(m) * G + G0 + g : m] : 1.f;
+      q4_store_planes(v, p.xmode == Q4X_INT8, xs, lane & 15, p.P, M, m, C, xf + g * 8 * C, xsg + g * 8 * NT,
+                      xsum + g * 8 * NT, live);
     }
   }
   __syncthreads();
 
-  for (int blk = cluster; blk < p.nblocks; blk += nclusters) {
+  bool ok = true;
+  int slot = 0;
+  uint32_t phase = 0;
+  int done = 0;
+  for (int ib = 0; ib < mine; ++ib) {
+    const int64_t row0 = static_cast<int64_t>(cluster + ib * nclusters) * R;
     float acc[TPW][NT][4];
 #pragma unroll
     for (int tt = 0; tt < TPW; ++tt)
@@ -282,109 +345,136 @@ __global__ void __launch_bounds__(kQ4DecMaxThreads, 1) q4_decode_kernel(const Q4
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[tt][t][e] = 0.f;
-    for (int j = 0; j < nstep; ++j) {
-      uint4 cw[GP][TPW][2];
-      float cs[GP][TPW][2];
+    // scales of this lane's rows (rho, rho + 8 of each tile), fetched a box ahead
+    const int64_t srow = row0 + wt * p.rw + rho;
+    const uint16_t* sbase = p.scales + srow * G + G0;
+    const int64_t left = min(p.N - srow, static_cast<int64_t>(p.rw - rho));  // rows from rho on
+    uint16_t sn[2][2 * TPW];
+    auto load_scales = [&](int j) {
+      const int g = 2 * (wk + p.Wk * j);
 #pragma unroll
-      for (int gg = 0; gg < GP; ++gg)
+      for (int h = 0; h < 2 * TPW; ++h) {
+        sn[0][h] = 8 * h < left ? __ldg(sbase + static_cast<int64_t>(8 * h) * G + g) : uint16_t(0);
+        sn[1][h] = 8 * h < left && g + 1 < Gn ? __ldg(sbase + static_cast<int64_t>(8 * h) * G + g + 1) : uint16_t(0);
+      }
+    };
+    if (nb > 0) load_scales(0);
+    for (int j = 0; j < nb && ok; ++j) {
+      float sc[2][2 * TPW];
 #pragma unroll
-        for (int h = 0; h < 2 * TPW; ++h) {
-          cw[gg][h >> 1][h & 1] = w[gg][h >> 1][h & 1];
-          cs[gg][h >> 1][h & 1] = __half2float(__ushort_as_half(sc[gg][h >> 1][h & 1]));
-        }
-      // the next step's loads, over the end of the block
-      if (j + 1 < nstep)
-        load(blk, j + 1);
-      else if (blk + nclusters < p.nblocks)
-        load(blk + nclusters, 0);
+      for (int h = 0; h < 4 * TPW; ++h)
+        sc[h & 1][h >> 1] = __half2float(__ushort_as_half(sn[h & 1][h >> 1]));
+      if (j + 1 < nb) load_scales(j + 1);
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars[slot], phase, FAULT_WAIT_FULL))) {
+        ok = false;
+        break;
+      }
+      const uint8_t* box = ring + slot * kBox + rho * 128;
+      const int g0 = 2 * (wk + p.Wk * j);
 #pragma unroll
-      for (int gg = 0; gg < GP; ++gg) {
-        const int g = (j * p.Wk + wk) * GP + gg;
+      for (int gg = 0; gg < 2; ++gg) {
+        const int g = g0 + gg;
         if (g >= Gn) break;  // the whole warp
-        float d[TPW][NT][4];
-#pragma unroll
-        for (int tt = 0; tt < TPW; ++tt)
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) d[tt][t][e] = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint4 b[NT];
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-            b[t] = 8 * t + r < M ? xf[(g * 4 + i) * 4 * M + 32 * t + lane] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-          for (int tt = 0; tt < TPW; ++tt) {
-            const uint32_t lo = (&cw[gg][tt][0].x)[i], hi = (&cw[gg][tt][1].x)[i];
-            uint32_t a0 = q4_pair<TX, 0>(lo), a1 = q4_pair<TX, 0>(hi), a2 = q4_pair<TX, 1>(lo), a3 = q4_pair<TX, 1>(hi);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) mma16816<TX>(d[tt][t], a0, a1, a2, a3, b[t].x, b[t].y);
-            a0 = q4_pair<TX, 2>(lo), a1 = q4_pair<TX, 2>(hi), a2 = q4_pair<TX, 3>(lo), a3 = q4_pair<TX, 3>(hi);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) mma16816<TX>(d[tt][t], a0, a1, a2, a3, b[t].z, b[t].w);
-          }
-        }
+        const uint4* xg = xf + g * 8 * C + lane;
+        uint4 b[NT][2];
+        int2 d0[NT];
+        float2 f[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          float f0 = 1.f, f1 = 1.f;
-          if constexpr (XG) {
-            const float2 f = *reinterpret_cast<const float2*>(xsg + g * 8 * NT + 8 * t + 2 * c);
-            f0 = f.x;
-            f1 = f.y;
+          const bool col = 8 * t + r < C;
+          b[t][0] = col ? xg[32 * t] : make_uint4(0, 0, 0, 0);
+          b[t][1] = col ? xg[4 * C + 32 * t] : make_uint4(0, 0, 0, 0);
+          d0[t] = *reinterpret_cast<const int2*>(xsum + g * 8 * NT + 8 * t + 2 * c);
+          f[t] = *reinterpret_cast<const float2*>(xsg + g * 8 * NT + 8 * t + 2 * c);
+        }
+#pragma unroll
+        for (int tt = 0; tt < TPW; ++tt) {
+          const int at = 16 * ((4 * gg + c) ^ rho);  // the 128-byte swizzle of a box row
+          const uint4 lo = *reinterpret_cast<const uint4*>(box + tt * 2048 + at);
+          const uint4 hi = *reinterpret_cast<const uint4*>(box + tt * 2048 + 1024 + at);
+          int d[NT][4];
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            d[t][0] = d[t][2] = d0[t].x;
+            d[t][1] = d[t][3] = d0[t].y;
           }
 #pragma unroll
-          for (int tt = 0; tt < TPW; ++tt) {
-            const float s0 = cs[gg][tt][0], s1 = cs[gg][tt][1];
-            acc[tt][t][0] += (XG ? s0 * f0 : s0) * d[tt][t][0];
-            acc[tt][t][1] += (XG ? s0 * f1 : s0) * d[tt][t][1];
-            acc[tt][t][2] += (XG ? s1 * f0 : s1) * d[tt][t][2];
-            acc[tt][t][3] += (XG ? s1 * f1 : s1) * d[tt][t][3];
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t wl = (&lo.x)[i], wh = (&hi.x)[i];
+            const uint32_t a0 = wl & 0x0F0F0F0Fu, a1 = wh & 0x0F0F0F0Fu;
+            const uint32_t a2 = (wl >> 4) & 0x0F0F0F0Fu, a3 = (wh >> 4) & 0x0F0F0F0Fu;
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+              mma_u8s8(d[t], a0, a1, a2, a3, (&b[t][i >> 1].x)[2 * (i & 1)], (&b[t][i >> 1].x)[2 * (i & 1) + 1]);
+          }
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            const float s0 = sc[gg][2 * tt], s1 = sc[gg][2 * tt + 1];
+            acc[tt][t][0] += s0 * f[t].x * (__int_as_float(d[t][0]) - kQ4Magic);
+            acc[tt][t][1] += s0 * f[t].y * (__int_as_float(d[t][1]) - kQ4Magic);
+            acc[tt][t][2] += s1 * f[t].x * (__int_as_float(d[t][2]) - kQ4Magic);
+            acc[tt][t][3] += s1 * f[t].y * (__int_as_float(d[t][3]) - kQ4Magic);
           }
         }
       }
+      __syncwarp();  // every lane has read the box
+      ++done;
+      if (lane == 0 && done + p.slots <= total) fetch();
+      if (++slot == p.slots) {
+        slot = 0;
+        phase ^= 1u;
+      }
     }
-    // partial sums [wk][token][row], joined over wk and then over the cluster
-    if (active) {
+    // partial sums [wk][column][row], joined over wk, the planes and the cluster
+    const int rows = 16 * TPW * p.Wt;
+    if (mine == 1) __syncthreads();  // they may lie over x'
+    if (wk < p.Wk) {
 #pragma unroll
       for (int tt = 0; tt < TPW; ++tt)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int m = 8 * t + 2 * c + (e & 1);
-            if (m < M) part[(wk * M + m) * rows + 16 * (TPW * wt + tt) + r + 8 * (e >> 1)] = acc[tt][t][e];
+            const int n = 8 * t + 2 * c + (e & 1);
+            if (n < C) part[(wk * C + n) * rows + 16 * (TPW * wt + tt) + rho + 8 * (e >> 1)] = acc[tt][t][e];
           }
     }
     __syncthreads();
-    const int64_t row0 = static_cast<int64_t>(blk) * p.R;
-    const int nr = static_cast<int>(min(static_cast<int64_t>(p.R), p.N - row0));
+    auto joined = [&](int m, int at) {
+      float v = 0.f;
+      for (int n = m; n < C; n += M)
+        for (int q = 0; q < p.Wk; ++q) v += part[(q * C + n) * rows + at];
+      return v;
+    };
+    const int T = 32 * kQ4DecWarps;
     if (p.S > 1) {
-      for (int o = tid; o < M * rows; o += T) {
-        float v = part[o];
-        for (int q = 1; q < p.Wk; ++q) v += part[q * M * rows + o];
-        part[o] = v;
-      }
+      // first plane's slots of warp class 0 take the CTA's sums (each is read by its writer only)
+      for (int o = tid; o < M * rows; o += T) part[o] = joined(o / rows, o % rows);
       cluster_sync_all();
     }
-    const int terms = p.S > 1 ? p.S : p.Wk;
-    for (int o = tid * p.S + rank; o < M * nr; o += T * p.S) {
-      const int m = o / nr, row = o - m * nr, at = m * rows + row;
-      float v;
+    for (int o = tid * p.S + rank; o < M * R; o += T * p.S) {
+      const int m = o / R, row = o - m * R;
+      const int w = row / p.rw, at = 16 * TPW * w + row - w * p.rw;
+      if (row0 + row >= p.N) continue;
+      float v = 0.f;
       if (p.S > 1) {
-        v = 0.f;
-        for (int q = 0; q < terms; ++q) v += ld_cluster_f32(cluster_map(smem_u32(part + at), q));
+        for (int q = 0; q < p.S; ++q) v += ld_cluster_f32(cluster_map(smem_u32(part + m * rows + at), q));
       } else {
-        v = part[at];
-        for (int q = 1; q < terms; ++q) v += part[q * M * rows + at];
+        v = joined(m, at);
       }
-      if (p.factor != nullptr) v *= __ldcg(p.factor + m);
       store_from_f32(p.y, m * p.N + row0 + row, p.yt, v);
     }
     if (p.S > 1)
       cluster_sync_all();  // no CTA overwrites (or leaves) what its peers still read
     else
       __syncthreads();
+  }
+  // after a wait that gave up: the copies still in flight land before the CTA leaves
+  if (!ok && lane == 0) {
+    for (int s = 0; s < p.slots && s < total - done; ++s) {
+      const int at = slot + s;
+      mbar_wait(&bars[at % p.slots], phase ^ (at >= p.slots ? 1u : 0u), FAULT_WAIT_FULL);
+    }
   }
 }
 

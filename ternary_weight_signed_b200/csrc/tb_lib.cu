@@ -1123,7 +1123,12 @@ bool is_8bit_dtype(int t) { return t == TB_INT8 || t == TB_E4M3; }
 
 // x' as fp16 [M, K], then the tokens' factors, padded to whole token tiles.
 size_t q4_x_bytes(int64_t M, int64_t K) { return (static_cast<size_t>(M) * K * 2 + 255) & ~static_cast<size_t>(255); }
-size_t q4_required_ws(int64_t M, int64_t K) { return q4_x_bytes(M, K) + static_cast<size_t>((M + 255) / 256) * 1024; }
+size_t q4_required_ws(int64_t M, int64_t K) {
+  const size_t gemm = q4_x_bytes(M, K) + static_cast<size_t>((M + 255) / 256) * 1024;
+  // the decode kernel's image: the planes, their factors and sums
+  const size_t image = M <= kQ4DecMaxM ? static_cast<size_t>(K / 128) * (3 * M) * (128 + 8) : 0;
+  return std::max(gemm, (image + 255) & ~static_cast<size_t>(255));
+}
 
 bool q4_sizes_ok(int64_t M, int64_t N, int64_t K) {
   return M >= 1 && N >= 1 && K >= 128 && K % 128 == 0 && M <= kMaxDim && N < (int64_t(1) << 30) && K <= kMaxDim &&
@@ -1214,60 +1219,60 @@ tb_status run_q4_gemm(const Q4Args& a, const DevInfo* d) {
 }
 
 struct Q4DecodePlan {
-  int threads, R, nblocks, Wt, Wk, TPW, S, Gs, clusters;
+  int NT, TPW, C, P, rw, nblocks, Wt, Wk, S, Gs, slots, clusters, part_at;
   size_t smem;
 };
 
-// Geometry of the decode kernel, by an estimate of the issue slots that the
-// busiest SM spends: a 16-row tile of a 128-group costs about 96 instructions
-// and an MMA per token tile and 16 codes, its activations about 20 per token
-// tile; staging x' costs its bytes.  Two CTAs of 8 warps on an SM, or one of 16.
-// False if x' of a cluster's slice does not fit.
-bool q4_decode_plan(int64_t M64, int64_t N, int64_t K, bool xg, int sm_count, int max_smem, Q4DecodePlan* out) {
-  if (M64 > kQ4DecMaxM) return false;
-  const int M = static_cast<int>(M64), NT = (M + 7) / 8, G = static_cast<int>(K / 128);
-  double best = -1;
-  for (int W = 8; W <= 16; W += 8) {
-    const int cps = W == 8 ? 2 : 1;
-    const int64_t budget = cps == 2 ? (max_smem - 1024) / 2 - 1024 : max_smem;
-    for (int S = 1; S <= 8; S *= 2) {
-      if (S > 1 && G < 2 * S) break;
-      const int Gs = (G + S - 1) / S;
+// Geometry of the decode kernel for C columns of x planes; false if they do not
+// fit.  Two CTAs an SM where x' leaves room, else one; the smallest cluster (K
+// split) whose slice fits; then the split of the 8 warps over rows and K that
+// gives the busiest warp the fewest 16-row tiles.
+bool q4_decode_plan(int64_t N, int64_t K, int C, int P, int sm_count, int max_smem, Q4DecodePlan* out) {
+  const int NT = (C + 7) / 8, G = static_cast<int>(K / 128);
+  if (NT > 4) return false;
+  for (int S = 1; S <= 8; S *= 2) {
+    const int Gs = ((G + S - 1) / S + 1) & ~1;
+    for (int cps = 2; cps >= 1; --cps) {
+      const int64_t budget = cps == 2 ? (max_smem + 1024) / 2 - 1024 : max_smem;
       const int clusters = std::max(1, sm_count * cps / S);
-      for (int TPW = 1; TPW <= (NT == 1 ? 4 : 2); ++TPW) {
-        if (TPW == 3) continue;
-        const int GP = q4_dec_gp(TPW);
-        for (int Wt = 1; Wt <= W; ++Wt) {
-          const int Wk = W / Wt, rows = 16 * TPW * Wt;
-          const int64_t smem = q4_dec_x_bytes(M, Gs) + q4_dec_xs_bytes(M, Gs, xg) + q4_dec_part_bytes(M, rows, Wk);
-          if (smem > budget) continue;
-          const int64_t rounds = (N + static_cast<int64_t>(rows) * clusters - 1) / (static_cast<int64_t>(rows) * clusters);
-          const int64_t R = (N + clusters * rounds - 1) / (clusters * rounds);
-          const double step = GP * (TPW * (96.0 + 8 * NT) + 20.0 * NT);
-          const int64_t steps = (Gs + Wk * GP - 1) / (Wk * GP);
-          const double issue = cps * W / 4.0 * (rounds * steps * step) * (Wt * Wk) / W;
-          const double sums = cps * static_cast<double>(rounds) * R * M * Wk / 16.0 * (S > 1 ? 2 : 1);
-          const double stage = cps * static_cast<double>(M) * Gs * 256 / 32.0;
-          const double cost = issue + sums + stage + (S > 1 ? 1500.0 * rounds : 0.0);
-          if (best < 0 || cost < best) {
-            best = cost;
-            *out = Q4DecodePlan{32 * W, static_cast<int>(R), static_cast<int>((N + R - 1) / R), Wt, Wk, TPW, S, Gs,
-                                clusters, static_cast<size_t>(smem)};
-          }
-        }
+      int64_t best = -1;
+      for (int Wt = 1; Wt <= kQ4DecWarps; Wt *= 2) {
+        const int Wk = kQ4DecWarps / Wt;
+        const int64_t per = static_cast<int64_t>(clusters) * Wt;  // warp rows boxes in a round
+        const int64_t rounds = (N + 32 * per - 1) / (32 * per);
+        const int rw = static_cast<int>((N + per * rounds - 1) / (per * rounds));
+        const int TPW = rw > 16 ? 2 : 1, rows = 16 * TPW * Wt;
+        const int64_t nblocks = (N + static_cast<int64_t>(Wt) * rw - 1) / (static_cast<int64_t>(Wt) * rw);
+        const int64_t x = q4_dec_x_bytes(C, Gs) + q4_dec_f_bytes(C, Gs) + 8 * kQ4DecWarps * kQ4DecSlots;
+        const int64_t part = q4_dec_part_bytes(C, rows, Wk);
+        const int64_t fixed = 1024 + (nblocks <= clusters ? std::max(x, part) : x + part);
+        const int64_t left = budget - fixed;
+        const int slots = static_cast<int>(std::min<int64_t>(kQ4DecSlots, left / q4_dec_ring_bytes(TPW, 1)));
+        if (left <= 0 || slots < 2) continue;
+        const int64_t boxes = ((Gs + 1) / 2 + Wk - 1) / Wk;
+        const int64_t cost = rounds * (boxes * 2 * TPW + 2);
+        if (best >= 0 && cost >= best) continue;
+        best = cost;
+        const int64_t ring = q4_dec_ring_bytes(TPW, slots);
+        *out = Q4DecodePlan{NT, TPW, C, P, rw, static_cast<int>(nblocks), Wt, Wk, S, Gs, slots, clusters,
+                            static_cast<int>(nblocks <= clusters ? ring : ring + x),
+                            static_cast<size_t>(ring + fixed)};
       }
+      if (best >= 0) return true;
+      if (G <= 2 * S) break;  // no finer split of K
     }
   }
-  return best >= 0;
+  return false;
 }
 
-template <int NT, int TPW, typename TX, bool XG>
-tb_status launch_q4_decode(const Q4DecodeParams& p, const Q4DecodePlan& pl, const DevInfo* d, cudaStream_t st) {
-  auto k = q4_decode_kernel<NT, TPW, TX, XG>;
+template <int NT, int TPW>
+tb_status launch_q4_decode(const CUtensorMap& tm, const Q4DecodeParams& p, const Q4DecodePlan& pl, const DevInfo* d,
+                           cudaStream_t st) {
+  auto k = q4_decode_kernel<NT, TPW>;
   if (allow_smem(k, d) != TB_OK) return TB_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(pl.S * std::min(pl.clusters, pl.nblocks)));
-  cfg.blockDim = dim3(static_cast<unsigned>(pl.threads));
+  cfg.blockDim = dim3(32 * kQ4DecWarps);
   cfg.dynamicSmemBytes = pl.smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -1279,65 +1284,68 @@ tb_status launch_q4_decode(const Q4DecodeParams& p, const Q4DecodePlan& pl, cons
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pl.S > 1 ? 2 : 1;
-  if (cudaLaunchKernelEx(&cfg, k, p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, k, tm, p) != cudaSuccess) {
     cudaGetLastError();
     return TB_ERR_CUDA;
   }
   return TB_OK;
 }
 
-template <int NT, typename TX, bool XG>
-tb_status launch_q4_decode_tiles(const Q4DecodeParams& p, const Q4DecodePlan& pl, const DevInfo* d, cudaStream_t st) {
-  if constexpr (NT == 1) {
-    if (pl.TPW == 4) return launch_q4_decode<NT, 4, TX, XG>(p, pl, d, st);
-  }
-  return pl.TPW == 2 ? launch_q4_decode<NT, 2, TX, XG>(p, pl, d, st) : launch_q4_decode<NT, 1, TX, XG>(p, pl, d, st);
-}
-
 tb_status run_q4_decode(const Q4Args& a, const DevInfo* d, const Q4DecodePlan& pl) {
   Q4DecodeParams p;
   p.x = a.x;
+  p.x_scales = a.x_scales;
   p.xmode = a.xt == TB_BF16 ? Q4X_BF16 : (a.xt == TB_FP16 ? Q4X_FP16 : (a.xt == TB_INT8 ? Q4X_INT8 : Q4X_E4M3));
-  const bool xg = is_8bit_dtype(a.xt) && a.x_group == 128;
-  p.group_scales = xg ? a.x_scales : nullptr;
-  p.factor = xg ? nullptr : a.x_scales;
-  if (a.signs != nullptr) {
-    __half* xh = static_cast<__half*>(a.ws);
-    float* factor = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + q4_x_bytes(a.M, a.K));
-    const tb_status st = run_q4_prep(a, xh, factor);
-    if (st != TB_OK) return st;
-    p.x = xh;
-    p.xmode = Q4X_PREP;
-    p.factor = factor;
-  }
-  p.packed = a.packed;
+  p.x_group = static_cast<int>(a.x_group);
   p.scales = a.scales;
   p.y = a.y;
-  p.yt = a.yt;
-  p.M = static_cast<int>(a.M);
   p.N = a.N;
+  p.M = static_cast<int>(a.M);
   p.K = static_cast<int>(a.K);
-  p.R = pl.R;
+  p.yt = a.yt;
+  p.P = pl.P;
+  p.C = pl.C;
+  p.rw = pl.rw;
   p.nblocks = pl.nblocks;
   p.Wt = pl.Wt;
   p.Wk = pl.Wk;
   p.S = pl.S;
   p.Gs = pl.Gs;
-  const bool h = p.xmode != Q4X_BF16 && p.xmode != Q4X_INT8;  // int8 codes are exact in bf16, e4m3 ones in fp16
-  if (a.M <= 8) {
-    if (h) return xg ? launch_q4_decode_tiles<1, __half, true>(p, pl, d, a.st) : launch_q4_decode_tiles<1, __half, false>(p, pl, d, a.st);
-    return xg ? launch_q4_decode_tiles<1, __nv_bfloat16, true>(p, pl, d, a.st)
-              : launch_q4_decode_tiles<1, __nv_bfloat16, false>(p, pl, d, a.st);
+  p.slots = pl.slots;
+  p.part_at = pl.part_at;
+  CUtensorMap tm;
+  if (make_map_2d(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.packed, a.K / 2, a.N, a.K / 2, 128,
+                  static_cast<uint32_t>(pl.rw), CU_TENSOR_MAP_SWIZZLE_128B) != TB_OK)
+    return TB_ERR_CUDA;
+  if (a.M > kQ4DecInCta || a.signs != nullptr) {
+    uint4* image = static_cast<uint4*>(a.ws);
+    const int64_t G = a.K / 128;
+    float* factors = reinterpret_cast<float*>(image + G * 8 * pl.C);
+    q4_planes_kernel<<<dim3(static_cast<unsigned>((a.K + kHB - 1) / kHB), static_cast<unsigned>(a.M)), kHThreads, 0,
+                       a.st>>>(a.x, p.xmode, a.x_scales, p.x_group, a.signs, image, factors, p.M, p.K, pl.P, pl.C);
+    if (launch_status() != TB_OK) return TB_ERR_CUDA;
+    p.x = image;
+    p.x_scales = factors;
+    p.xmode = Q4X_IMAGE;
   }
-  if (h) return xg ? launch_q4_decode_tiles<2, __half, true>(p, pl, d, a.st) : launch_q4_decode_tiles<2, __half, false>(p, pl, d, a.st);
-  return xg ? launch_q4_decode_tiles<2, __nv_bfloat16, true>(p, pl, d, a.st)
-            : launch_q4_decode_tiles<2, __nv_bfloat16, false>(p, pl, d, a.st);
+#define TB_Q4D(NT) \
+  case NT: return pl.TPW == 2 ? launch_q4_decode<NT, 2>(tm, p, pl, d, a.st) : launch_q4_decode<NT, 1>(tm, p, pl, d, a.st);
+  switch (pl.NT) {
+    TB_Q4D(1)
+    TB_Q4D(2)
+    TB_Q4D(3)
+    default: return pl.TPW == 2 ? launch_q4_decode<4, 2>(tm, p, pl, d, a.st) : launch_q4_decode<4, 1>(tm, p, pl, d, a.st);
+  }
+#undef TB_Q4D
 }
 
 tb_status run_q4(const Q4Args& a, const DevInfo* d) {
   Q4DecodePlan pl;
-  const bool xg = is_8bit_dtype(a.xt) && a.x_group == 128;
-  if (q4_decode_plan(a.M, a.N, a.K, xg, d->sm_count, d->max_smem_optin, &pl)) return run_q4_decode(a, d, pl);
+  if (a.M <= kQ4DecMaxM) {
+    const int P = q4_planes(a.xt == TB_INT8 ? Q4X_INT8 : Q4X_BF16, static_cast<int>(a.M));
+    if (q4_decode_plan(a.N, a.K, P * static_cast<int>(a.M), P, d->sm_count, d->max_smem_optin, &pl))
+      return run_q4_decode(a, d, pl);
+  }
   return run_q4_gemm(a, d);
 }
 
