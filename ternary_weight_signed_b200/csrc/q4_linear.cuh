@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kHThreads)
 //     columns, exact: the codes c = q + 8 as they are (a mask and a shift, 3
 //     instructions for 8 codes), x' as 8-bit planes of a fixed-point number, a
 //     column per plane and token.  Every group has its own power of two: three
-//     planes hold a value to 2^-23 of its group's largest, two to 2^-15, and an int8
+//     planes hold a value to 2^-22 of its group's largest, two to 2^-15, and an int8
 //     is one.  The sums of a group start from -8 sum x, which takes the bias off,
 //     plus the bits of 1.5 2^23, which makes the integer sum a float's mantissa: one
 //     subtraction instead of a conversion.  The groups are added in fp32.
@@ -113,16 +113,16 @@ __global__ void __launch_bounds__(kHThreads)
 //     m16n8k16 f16 15.4, m16n8k32 s8 15.8, m16n8k32 e4m3 35 (no pipe of its own).
 //     tcgen05.mma with 128 rows takes 47-56 cycles an SM for any N up to 64, K = 16:
 //     36 weights a cycle against 128 / (columns / 8) here.
-//   * Each warp streams its own rows: boxes of up to 32 rows x 128 bytes (256
+//   * Each warp streams its own rows: boxes of up to 16 rows x 128 bytes (256
 //     codes) by TMA into a ring of its own, refilled by the warp itself, so no warp
 //     waits for another inside the loop.  K is spread over Wk of a CTA's warps
 //     (fp32 partial sums joined in shared memory in a fixed order) and, when x' does
 //     not fit one CTA, over the S CTAs of a cluster, which read each other's partial
 //     sums through distributed shared memory.  No atomics: the bits do not depend on
 //     scheduling.
-constexpr int kQ4DecWarps = 8;
+constexpr int kQ4DecWarps = 16;      // of a CTA, one CTA an SM
 constexpr int kQ4DecMaxM = 16;
-constexpr int kQ4DecSlots = 4;       // boxes in flight a warp, at most
+constexpr int kQ4DecSlots = 2;       // boxes in flight a warp; 3 and 4 delay the loads of x behind them: 13.0 -> 13.8 us
 constexpr int kQ4DecInCta = 4;       // tokens whose planes every CTA makes itself
 
 constexpr int kQ4MagicBits = 0x4B400000;   // 1.5 2^23; adding an integer below 2^22 to the bits adds it to the value
@@ -144,61 +144,78 @@ struct Q4DecodeParams {
   int rw, nblocks;  // rows of a warp's box; row blocks of Wt rw rows (a cluster takes every nclusters-th)
   int Wt, Wk;       // row classes x K classes of a CTA's warps
   int S, Gs;        // cluster size, 128-groups of a CTA's K slice (even)
-  int slots;        // ring of a warp
   int part_at;      // byte offset of the partial sums in shared memory
 };
 
-__host__ __device__ constexpr int q4_dec_box_bytes(int tpw) { return 16 * tpw * 128; }
+constexpr int kQ4DecBoxRows = 16;
+constexpr int kQ4DecBoxBytes = kQ4DecBoxRows * 128;
 // shared memory: rings | x planes [Gs][2][C][4] x 16 bytes | factors, sums [Gs][8 NT] each | barriers | partial sums
-__host__ __device__ constexpr int64_t q4_dec_ring_bytes(int tpw, int slots) {
-  return int64_t(kQ4DecWarps) * slots * q4_dec_box_bytes(tpw);
-}
+constexpr int kQ4DecRingBytes = kQ4DecWarps * kQ4DecSlots * kQ4DecBoxBytes;
 __host__ __device__ constexpr int64_t q4_dec_x_bytes(int C, int Gs) { return int64_t(128) * C * Gs; }
 __host__ __device__ constexpr int64_t q4_dec_f_bytes(int C, int Gs) { return int64_t(64) * ((C + 7) / 8) * Gs; }
 __host__ __device__ constexpr int64_t q4_dec_part_bytes(int C, int rows, int Wk) { return int64_t(4) * Wk * C * rows; }
 
-// Planes, factors and sums of 8 consecutive values v (place q = 4 c + i of a
-// 128-group: codes 32 c + 8 i ..) of one token; the 16 lanes that hold the group
-// call this together (a whole warp at a time; lanes without a group of their own
-// are not live and store nothing).  xs multiplies the group's values.  Column n
-// of the group goes to dst[(i / 2) C 4 + 4 n + c], half i % 2.
-__device__ __forceinline__ void q4_store_planes(float v[8], bool int8, float xs, int q, int P, int M, int m, int C,
+// Planes, factors and sums of a 128-group of one token, 32 consecutive values v a
+// lane: lane c of the four that call this together holds the codes 32 c ..; lanes
+// without a group of their own are not live and store nothing.  xs multiplies the
+// group's values.  Column n of the group goes to dst[h C 4 + 4 n + c], h the half
+// of the lane's codes.
+__device__ __forceinline__ void q4_store_planes(const float (&v)[32], bool int8, float xs, int P, int M, int m, int C,
                                                 uint4* dst, float* fdst, int* sdst, bool live) {
+  const int c = threadIdx.x & 3;
   float f = 1.f, inv = 1.f;
   if (!int8) {
     uint32_t mb = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) mb = max(mb, abs_bits(v[j]));
-#pragma unroll
-    for (int o = 1; o < 16; o <<= 1) mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, o));
-    // the largest under 2^top (1.9921 2^(top - 1): the highest plane stays under 128)
-    const int top = 8 * P - 1;
-    const int e = min(max(static_cast<int>((mb + 0x10200u) >> 23) - 127, -100), 128);
-    f = __uint_as_float(static_cast<uint32_t>(127 + top - 1 - e) << 23);
-    inv = mb >= kInfBits ? __uint_as_float(0x7FC00000u) : __uint_as_float(static_cast<uint32_t>(127 - top + 1 + e) << 23);
+    for (int j = 0; j < 32; ++j) mb = max(mb, abs_bits(v[j]));
+    mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
+    mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
+    // the largest under 2^22 (three planes) or 1.9921 2^14 (two: the higher one stays under 128)
+    const int top = P == 3 ? 21 : 14;
+    const int e = min(max(static_cast<int>((mb + (P == 3 ? 0u : 0x10200u)) >> 23) - 127, -100), 128);
+    f = __uint_as_float(static_cast<uint32_t>(127 + top - e) << 23);
+    inv = mb >= kInfBits ? __uint_as_float(0x7FC00000u) : __uint_as_float(static_cast<uint32_t>(127 - top + e) << 23);
   }
-  int x[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) x[j] = __float2int_rn(v[j] * f);
   inv *= xs;
-  const int c = q >> 2, i = q & 3;
-  for (int p = P - 1; p >= 0; --p) {
-    uint32_t w[2] = {0u, 0u};  // bytes (0, 2, 4, 6) and (1, 3, 5, 7)
+  int s[3] = {0, 0, 0};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      w[j & 1] |= (static_cast<uint32_t>(x[j]) & 0xFFu) << (8 * (j >> 1));
-      x[j] = (x[j] + 128) >> 8;
-    }
-    int s = __dp4a(static_cast<int>(w[0]), 0x01010101, __dp4a(static_cast<int>(w[1]), 0x01010101, 0));
+  for (int h = 0; h < 2; ++h) {
+    uint32_t w[3][4];
 #pragma unroll
-    for (int o = 1; o < 16; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const int n = p * M + m;
-    if (live) {
-      reinterpret_cast<uint2*>(dst + (i >> 1) * 4 * C + 4 * n + c)[i & 1] = make_uint2(w[0], w[1]);
-      if (q == 0) {
-        fdst[n] = inv;
-        sdst[n] = kQ4MagicBits - 8 * s;
+    for (int i = 0; i < 2; ++i) {
+      // nearest integers as the mantissas of 1.5 2^23 + v f, then their signed
+      // base-256 digits: with 128 added to every digit they are the bytes, and
+      // flipping the top bits takes it off again
+      uint32_t x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        x[j] = (__float_as_uint(fmaf(v[16 * h + 8 * i + j], f, kQ4Magic)) +
+                (0x00808080u - static_cast<uint32_t>(kQ4MagicBits))) ^ 0x00808080u;
+      // byte p of the values (0, 2, 4, 6) and (1, 3, 5, 7): 4 x 4 byte transposes
+#pragma unroll
+      for (int o = 0; o < 2; ++o) {
+        const uint32_t lo = __byte_perm(x[o], x[o + 2], 0x5140), hi = __byte_perm(x[o + 4], x[o + 6], 0x5140);
+        w[0][2 * i + o] = __byte_perm(lo, hi, 0x5410);
+        w[1][2 * i + o] = __byte_perm(lo, hi, 0x7632);
+        w[2][2 * i + o] =
+            __byte_perm(__byte_perm(x[o], x[o + 2], 0x0062), __byte_perm(x[o + 4], x[o + 6], 0x0062), 0x5410);
       }
+    }
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {  // plane p: digit p, column P - 1 - p of the token
+#pragma unroll
+      for (int o = 0; o < 4; ++o) s[p] = __dp4a(static_cast<int>(w[p][o]), 0x01010101, s[p]);
+      if (p < P && live) dst[h * 4 * C + 4 * ((P - 1 - p) * M + m) + c] = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+    }
+  }
+#pragma unroll
+  for (int p = 0; p < 3; ++p) {
+    s[p] += __shfl_xor_sync(0xffffffffu, s[p], 1);
+    s[p] += __shfl_xor_sync(0xffffffffu, s[p], 2);
+    if (p < P && live && c == 0) {
+      const int n = (P - 1 - p) * M + m;
+      fdst[n] = inv;
+      sdst[n] = kQ4MagicBits - 8 * s[p];
     }
     inv *= 256.f;
   }
@@ -215,18 +232,19 @@ __device__ __forceinline__ void q4_load8_any(const void* x, int64_t at, int xmod
 
 // The planes of all tokens, once for the whole grid of the decode kernel (more
 // than kQ4DecInCta tokens, or a rotated x): image [G][2][C][4] x 16 bytes, then
-// factors and sums, [G][C] each.  grid (ceil(K / 1024), M), 128 threads.
+// factors and sums, [G][C] each.  grid (ceil(K / 1024), M), 128 threads: they
+// load (and rotate) 8 values each, and the first 32 make the planes of the
+// block's eight groups.
 __global__ void __launch_bounds__(kHThreads)
     q4_planes_kernel(const void* __restrict__ x, int xmode, const float* __restrict__ x_scales, int group,
                      const int8_t* __restrict__ signs, uint4* __restrict__ image, float* __restrict__ factors, int M,
                      int K, int P, int C) {
-  __shared__ float sm[kHB];
+  __shared__ __align__(16) float sm[kHB + 8 * 32];  // 32 values and 8 of padding a lane
   pdl_launch_dependents();
   const int tid = threadIdx.x, m = blockIdx.y, G = K / 128;
   const int k = blockIdx.x * kHB + 8 * tid;
-  const bool in = k < K;  // K % 128 == 0: whole groups of 16 threads
   float v[8] = {};
-  if (in) q4_load8_any(x, static_cast<int64_t>(m) * K + k, xmode, v);
+  if (k < K) q4_load8_any(x, static_cast<int64_t>(m) * K + k, xmode, v);
   if (signs != nullptr) {
     float d[8];
     load_signs8(signs + k, d);
@@ -236,12 +254,19 @@ __global__ void __launch_bounds__(kHThreads)
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] *= kHNorm;
   }
-  const int g = in ? k >> 7 : 0;
+  store8<float>(sm + 40 * (tid >> 2) + 8 * (tid & 3), v);
+  __syncthreads();
+  if (tid >= 32) return;
+  float u[32];
+#pragma unroll
+  for (int j = 0; j < 32; j += 8) load8<float>(sm + 40 * tid + j, u + j);
+  const bool live = blockIdx.x * kHB + 32 * tid < K;  // K % 128 == 0: whole groups of four lanes
+  const int g = live ? blockIdx.x * 8 + (tid >> 2) : 0;
   const bool x8 = xmode == Q4X_INT8 || xmode == Q4X_E4M3;
   const float xs = x8 ? x_scales[group == 128 ? static_cast<int64_t>(m) * G + g : m] : 1.f;
-  q4_store_planes(v, xmode == Q4X_INT8, xs, tid & 15, P, M, m, C, image + static_cast<int64_t>(g) * 8 * C,
+  q4_store_planes(u, xmode == Q4X_INT8, xs, P, M, m, C, image + static_cast<int64_t>(g) * 8 * C,
                   factors + static_cast<int64_t>(g) * C,
-                  reinterpret_cast<int*>(factors + static_cast<int64_t>(G + g) * C), in);
+                  reinterpret_cast<int*>(factors + static_cast<int64_t>(G + g) * C), live);
 }
 
 // c += a b, a: 16 x 32 unsigned, b: 32 x 8 signed bytes.
@@ -259,21 +284,21 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   return v;
 }
 
-// NT: column tiles of 8; TPW: 16-row tiles of a warp's box.
-template <int NT, int TPW>
-__global__ void __launch_bounds__(32 * kQ4DecWarps, 2)
+// NT: column tiles of 8.
+template <int NT>
+__global__ void __launch_bounds__(32 * kQ4DecWarps, 1)
     q4_decode_kernel(const __grid_constant__ CUtensorMap tm_w, const Q4DecodeParams p) {
-  constexpr int kBox = q4_dec_box_bytes(TPW);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int M = p.M, C = p.C, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int T = 32 * kQ4DecWarps;
   const int r = lane >> 2, c = lane & 3;
   const int rho = (r >> 1) + 4 * (r & 1);  // the fragment's row r is row rho of its 8: no bank conflict below
   const int rank = p.S > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int cluster = static_cast<int>(blockIdx.x) / p.S, nclusters = static_cast<int>(gridDim.x) / p.S;
   const int G = p.K >> 7, G0 = rank * p.Gs, Gn = max(0, min(p.Gs, G - G0));
-  uint8_t* ring = smem + warp * p.slots * kBox;
-  uint4* xf = reinterpret_cast<uint4*>(smem + q4_dec_ring_bytes(TPW, p.slots));
+  uint8_t* ring = smem + warp * kQ4DecSlots * kQ4DecBoxBytes;
+  uint4* xf = reinterpret_cast<uint4*>(smem + kQ4DecRingBytes);
   float* xsg = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(xf) + q4_dec_x_bytes(C, p.Gs));
   int* xsum = reinterpret_cast<int*>(xsg + p.Gs * 8 * NT);
   uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(xsg) + q4_dec_f_bytes(C, p.Gs)) +
@@ -293,41 +318,58 @@ __global__ void __launch_bounds__(32 * kQ4DecWarps, 2)
   auto fetch = [&]() {
     const int row = (cluster + fb * nclusters) * R + wt * p.rw;
     mbar_arrive_expect_tx(&bars[fs], bytes);
-    tma_load_2d(ring + fs * kBox, &tm_w, (G0 + 2 * (wk + p.Wk * fj)) * 64, row, &bars[fs]);
+    tma_load_2d(ring + fs * kQ4DecBoxBytes, &tm_w, (G0 + 2 * (wk + p.Wk * fj)) * 64, row, &bars[fs]);
     if (++fj == nb) {
       fj = 0;
       ++fb;
     }
-    if (++fs == p.slots) fs = 0;
+    if (++fs == kQ4DecSlots) fs = 0;
   };
   if (lane == 0) {
-    for (int s = 0; s < p.slots; ++s) mbar_init(&bars[s], 1);
+    for (int s = 0; s < kQ4DecSlots; ++s) mbar_init(&bars[s], 1);
     fence_mbar_init();
-    for (int s = 0; s < p.slots && s < total; ++s) fetch();  // weights do not wait for the previous kernel
+    for (int s = 0; s < kQ4DecSlots && s < total; ++s) fetch();  // weights do not wait for the previous kernel
   }
+  // scales of this lane's rows (rho, rho + 8), fetched a box ahead
+  uint16_t sn[2][2];
+  auto load_scales = [&](int ib, int j) {
+    const int64_t row = static_cast<int64_t>(cluster + ib * nclusters) * R + wt * p.rw + rho;
+    const int g = 2 * (wk + p.Wk * j);
+    const uint16_t* src = p.scales + row * G + G0 + g;
+    const int left = static_cast<int>(min(p.N - row, static_cast<int64_t>(p.rw - rho)));  // rows from rho on
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      sn[0][h] = 8 * h < left ? __ldg(src + 8 * h * G) : uint16_t(0);
+      sn[1][h] = 8 * h < left && g + 1 < Gn ? __ldg(src + 8 * h * G + 1) : uint16_t(0);
+    }
+  };
+  if (nb > 0) load_scales(0, 0);
   pdl_launch_dependents();
   pdl_wait();
   if (p.xmode == Q4X_IMAGE) {
     const uint4* src = static_cast<const uint4*>(p.x) + static_cast<int64_t>(G0) * 8 * C;
-    for (int q = tid; q < 8 * C * Gn; q += 32 * kQ4DecWarps) xf[q] = __ldcg(src + q);
-    for (int q = tid; q < C * Gn; q += 32 * kQ4DecWarps) {
+    for (int q = tid; q < 8 * C * Gn; q += T) xf[q] = __ldcg(src + q);
+    for (int q = tid; q < C * Gn; q += T) {
       const int g = q / C, n = q - g * C;
       xsg[g * 8 * NT + n] = __ldcg(p.x_scales + static_cast<int64_t>(G0) * C + q);
       xsum[g * 8 * NT + n] = __ldcg(reinterpret_cast<const int*>(p.x_scales) + static_cast<int64_t>(G + G0) * C + q);
     }
   } else {
-    // half a warp makes the planes of one token's group
+    // four lanes make the planes of one token's group
     const bool x8 = p.xmode == Q4X_INT8 || p.xmode == Q4X_E4M3;
     const int items = M * Gn;
-    for (int q0 = 2 * warp; q0 < items; q0 += 2 * kQ4DecWarps) {
-      const bool live = q0 + (lane >> 4) < items;
-      const int q = live ? q0 + (lane >> 4) : q0;
+    for (int q0 = 8 * warp; q0 < items; q0 += T / 4) {
+      const bool live = q0 + (lane >> 2) < items;
+      const int q = live ? q0 + (lane >> 2) : q0;
       const int m = q / Gn, g = q - m * Gn;
-      float v[8];
-      q4_load8_any(p.x, static_cast<int64_t>(m) * p.K + static_cast<int64_t>(G0 + g) * 128 + 8 * (lane & 15), p.xmode, v);
+      float v[32];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        q4_load8_any(p.x, static_cast<int64_t>(m) * p.K + static_cast<int64_t>(G0 + g) * 128 + 32 * c + 8 * j, p.xmode,
+                     v + 8 * j);
       const float xs = x8 ? p.x_scales[p.x_group == 128 ? static_cast<int64_t>(m) * G + G0 + g : m] : 1.f;
-      q4_store_planes(v, p.xmode == Q4X_INT8, xs, lane & 15, p.P, M, m, C, xf + g * 8 * C, xsg + g * 8 * NT,
-                      xsum + g * 8 * NT, live);
+      q4_store_planes(v, p.xmode == Q4X_INT8, xs, p.P, M, m, C, xf + g * 8 * C, xsg + g * 8 * NT, xsum + g * 8 * NT,
+                      live);
     }
   }
   __syncthreads();
@@ -338,43 +380,26 @@ __global__ void __launch_bounds__(32 * kQ4DecWarps, 2)
   int done = 0;
   for (int ib = 0; ib < mine; ++ib) {
     const int64_t row0 = static_cast<int64_t>(cluster + ib * nclusters) * R;
-    float acc[TPW][NT][4];
+    float acc[NT][4];
 #pragma unroll
-    for (int tt = 0; tt < TPW; ++tt)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[tt][t][e] = 0.f;
-    // scales of this lane's rows (rho, rho + 8 of each tile), fetched a box ahead
-    const int64_t srow = row0 + wt * p.rw + rho;
-    const uint16_t* sbase = p.scales + srow * G + G0;
-    const int64_t left = min(p.N - srow, static_cast<int64_t>(p.rw - rho));  // rows from rho on
-    uint16_t sn[2][2 * TPW];
-    auto load_scales = [&](int j) {
-      const int g = 2 * (wk + p.Wk * j);
-#pragma unroll
-      for (int h = 0; h < 2 * TPW; ++h) {
-        sn[0][h] = 8 * h < left ? __ldg(sbase + static_cast<int64_t>(8 * h) * G + g) : uint16_t(0);
-        sn[1][h] = 8 * h < left && g + 1 < Gn ? __ldg(sbase + static_cast<int64_t>(8 * h) * G + g + 1) : uint16_t(0);
-      }
-    };
-    if (nb > 0) load_scales(0);
+      for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
+    if (nb > 0 && ib > 0) load_scales(ib, 0);
     for (int j = 0; j < nb && ok; ++j) {
-      float sc[2][2 * TPW];
+      float sc[2][2];
 #pragma unroll
-      for (int h = 0; h < 4 * TPW; ++h)
-        sc[h & 1][h >> 1] = __half2float(__ushort_as_half(sn[h & 1][h >> 1]));
-      if (j + 1 < nb) load_scales(j + 1);
+      for (int h = 0; h < 4; ++h) sc[h & 1][h >> 1] = __half2float(__ushort_as_half(sn[h & 1][h >> 1]));
+      if (j + 1 < nb) load_scales(ib, j + 1);
       if (!__all_sync(0xffffffffu, mbar_wait(&bars[slot], phase, FAULT_WAIT_FULL))) {
         ok = false;
         break;
       }
-      const uint8_t* box = ring + slot * kBox + rho * 128;
+      const uint8_t* box = ring + slot * kQ4DecBoxBytes + rho * 128;
       const int g0 = 2 * (wk + p.Wk * j);
 #pragma unroll
       for (int gg = 0; gg < 2; ++gg) {
-        const int g = g0 + gg;
-        if (g >= Gn) break;  // the whole warp
+        const int g = min(g0 + gg, Gn - 1);  // past an odd end: any x', the scales are zero
         const uint4* xg = xf + g * 8 * C + lane;
         uint4 b[NT][2];
         int2 d0[NT];
@@ -387,80 +412,80 @@ __global__ void __launch_bounds__(32 * kQ4DecWarps, 2)
           d0[t] = *reinterpret_cast<const int2*>(xsum + g * 8 * NT + 8 * t + 2 * c);
           f[t] = *reinterpret_cast<const float2*>(xsg + g * 8 * NT + 8 * t + 2 * c);
         }
+        const int at = 16 * ((4 * gg + c) ^ rho);  // the 128-byte swizzle of a box row
+        const uint4 lo = *reinterpret_cast<const uint4*>(box + at);
+        const uint4 hi = *reinterpret_cast<const uint4*>(box + 1024 + at);
+        int d[NT][4];
 #pragma unroll
-        for (int tt = 0; tt < TPW; ++tt) {
-          const int at = 16 * ((4 * gg + c) ^ rho);  // the 128-byte swizzle of a box row
-          const uint4 lo = *reinterpret_cast<const uint4*>(box + tt * 2048 + at);
-          const uint4 hi = *reinterpret_cast<const uint4*>(box + tt * 2048 + 1024 + at);
-          int d[NT][4];
+        for (int t = 0; t < NT; ++t) {
+          d[t][0] = d[t][2] = d0[t].x;
+          d[t][1] = d[t][3] = d0[t].y;
+        }
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            d[t][0] = d[t][2] = d0[t].x;
-            d[t][1] = d[t][3] = d0[t].y;
-          }
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t wl = (&lo.x)[i], wh = (&hi.x)[i];
+          const uint32_t a0 = wl & 0x0F0F0F0Fu, a1 = wh & 0x0F0F0F0Fu;
+          const uint32_t a2 = (wl >> 4) & 0x0F0F0F0Fu, a3 = (wh >> 4) & 0x0F0F0F0Fu;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t wl = (&lo.x)[i], wh = (&hi.x)[i];
-            const uint32_t a0 = wl & 0x0F0F0F0Fu, a1 = wh & 0x0F0F0F0Fu;
-            const uint32_t a2 = (wl >> 4) & 0x0F0F0F0Fu, a3 = (wh >> 4) & 0x0F0F0F0Fu;
+          for (int t = 0; t < NT; ++t)
+            mma_u8s8(d[t], a0, a1, a2, a3, (&b[t][i >> 1].x)[2 * (i & 1)], (&b[t][i >> 1].x)[2 * (i & 1) + 1]);
+        }
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-              mma_u8s8(d[t], a0, a1, a2, a3, (&b[t][i >> 1].x)[2 * (i & 1)], (&b[t][i >> 1].x)[2 * (i & 1) + 1]);
-          }
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            const float s0 = sc[gg][2 * tt], s1 = sc[gg][2 * tt + 1];
-            acc[tt][t][0] += s0 * f[t].x * (__int_as_float(d[t][0]) - kQ4Magic);
-            acc[tt][t][1] += s0 * f[t].y * (__int_as_float(d[t][1]) - kQ4Magic);
-            acc[tt][t][2] += s1 * f[t].x * (__int_as_float(d[t][2]) - kQ4Magic);
-            acc[tt][t][3] += s1 * f[t].y * (__int_as_float(d[t][3]) - kQ4Magic);
-          }
+        for (int t = 0; t < NT; ++t) {
+          const float s0 = sc[gg][0], s1 = sc[gg][1];
+          acc[t][0] += s0 * f[t].x * (__int_as_float(d[t][0]) - kQ4Magic);
+          acc[t][1] += s0 * f[t].y * (__int_as_float(d[t][1]) - kQ4Magic);
+          acc[t][2] += s1 * f[t].x * (__int_as_float(d[t][2]) - kQ4Magic);
+          acc[t][3] += s1 * f[t].y * (__int_as_float(d[t][3]) - kQ4Magic);
         }
       }
       __syncwarp();  // every lane has read the box
       ++done;
-      if (lane == 0 && done + p.slots <= total) fetch();
-      if (++slot == p.slots) {
+      if (lane == 0 && done + kQ4DecSlots <= total) fetch();
+      if (++slot == kQ4DecSlots) {
         slot = 0;
         phase ^= 1u;
       }
     }
-    // partial sums [wk][column][row], joined over wk, the planes and the cluster
-    const int rows = 16 * TPW * p.Wt;
+    // partial sums [token][row][wk, plane], joined over warps, planes and the cluster
+    const int rows = kQ4DecBoxRows * p.Wt, terms = p.Wk * p.P;
     if (mine == 1) __syncthreads();  // they may lie over x'
     if (wk < p.Wk) {
 #pragma unroll
-      for (int tt = 0; tt < TPW; ++tt)
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int n = 8 * t + 2 * c + (e & 1);
-            if (n < C) part[(wk * C + n) * rows + 16 * (TPW * wt + tt) + rho + 8 * (e >> 1)] = acc[tt][t][e];
-          }
+        for (int e = 0; e < 2; ++e) {
+          const int n = 8 * t + 2 * c + e;
+          if (n >= C) continue;
+          const int pl = (n >= M) + (n >= 2 * M), m = n - pl * M;
+          float* dst = part + (m * rows + kQ4DecBoxRows * wt + rho) * terms + wk * p.P + pl;
+          dst[0] = acc[t][e];
+          dst[8 * terms] = acc[t][e + 2];
+        }
     }
     __syncthreads();
-    auto joined = [&](int m, int at) {
-      float v = 0.f;
-      for (int n = m; n < C; n += M)
-        for (int q = 0; q < p.Wk; ++q) v += part[(q * C + n) * rows + at];
+    auto joined = [&](int at) {
+      const float* s = part + at * terms;
+      float v = s[0];
+#pragma unroll 4
+      for (int q = 1; q < terms; ++q) v += s[q];
       return v;
     };
-    const int T = 32 * kQ4DecWarps;
     if (p.S > 1) {
-      // first plane's slots of warp class 0 take the CTA's sums (each is read by its writer only)
-      for (int o = tid; o < M * rows; o += T) part[o] = joined(o / rows, o % rows);
+      // the first term's place takes the CTA's sum (only its own thread reads it before)
+      for (int o = tid; o < M * rows; o += T) part[o * terms] = joined(o);
       cluster_sync_all();
     }
     for (int o = tid * p.S + rank; o < M * R; o += T * p.S) {
       const int m = o / R, row = o - m * R;
-      const int w = row / p.rw, at = 16 * TPW * w + row - w * p.rw;
+      const int w = row / p.rw, at = m * rows + kQ4DecBoxRows * w + row - w * p.rw;
       if (row0 + row >= p.N) continue;
-      float v = 0.f;
+      float v;
       if (p.S > 1) {
-        for (int q = 0; q < p.S; ++q) v += ld_cluster_f32(cluster_map(smem_u32(part + m * rows + at), q));
+        v = 0.f;
+        for (int q = 0; q < p.S; ++q) v += ld_cluster_f32(cluster_map(smem_u32(part + at * terms), q));
       } else {
-        v = joined(m, at);
+        v = joined(at);
       }
       store_from_f32(p.y, m * p.N + row0 + row, p.yt, v);
     }
@@ -471,9 +496,9 @@ __global__ void __launch_bounds__(32 * kQ4DecWarps, 2)
   }
   // after a wait that gave up: the copies still in flight land before the CTA leaves
   if (!ok && lane == 0) {
-    for (int s = 0; s < p.slots && s < total - done; ++s) {
+    for (int s = 0; s < kQ4DecSlots && s < total - done; ++s) {
       const int at = slot + s;
-      mbar_wait(&bars[at % p.slots], phase ^ (at >= p.slots ? 1u : 0u), FAULT_WAIT_FULL);
+      mbar_wait(&bars[at % kQ4DecSlots], phase ^ (at >= kQ4DecSlots ? 1u : 0u), FAULT_WAIT_FULL);
     }
   }
 }

@@ -1219,56 +1219,52 @@ tb_status run_q4_gemm(const Q4Args& a, const DevInfo* d) {
 }
 
 struct Q4DecodePlan {
-  int NT, TPW, C, P, rw, nblocks, Wt, Wk, S, Gs, slots, clusters, part_at;
+  int NT, C, P, rw, nblocks, Wt, Wk, S, Gs, clusters, part_at;
   size_t smem;
 };
 
-// Geometry of the decode kernel for C columns of x planes; false if they do not
-// fit.  Two CTAs an SM where x' leaves room, else one; the smallest cluster (K
-// split) whose slice fits; then the split of the 8 warps over rows and K that
-// gives the busiest warp the fewest 16-row tiles.
-bool q4_decode_plan(int64_t N, int64_t K, int C, int P, int sm_count, int max_smem, Q4DecodePlan* out) {
-  const int NT = (C + 7) / 8, G = static_cast<int>(K / 128);
+// Geometry of the decode kernel for C = P M columns of x planes; false if they
+// do not fit.  Whether two CTAs (a cluster) split K, and the split of the 16
+// warps over rows and K, are chosen by an estimate of the busiest warp's cycles,
+// from traces on B200: a 16-row tile of a 128-group about 300 plus 200 per column
+// tile, a round of row blocks 3000, the planes of 8 token-groups a warp 1200 (made
+// by the CTA) or 60 (copied),
+// a cluster's two barriers and remote sums 2500.  Clusters of 4 and 8 left SMs
+// empty and ran in two waves (16 x 5120 x 17408: 40 us against 21).
+bool q4_decode_plan(int64_t N, int64_t K, int M, int P, bool copied, int sm_count, int max_smem, Q4DecodePlan* out) {
+  const int C = P * M, NT = (C + 7) / 8, G = static_cast<int>(K / 128);
   if (NT > 4) return false;
-  for (int S = 1; S <= 8; S *= 2) {
-    const int Gs = ((G + S - 1) / S + 1) & ~1;
-    for (int cps = 2; cps >= 1; --cps) {
-      const int64_t budget = cps == 2 ? (max_smem + 1024) / 2 - 1024 : max_smem;
-      const int clusters = std::max(1, sm_count * cps / S);
-      int64_t best = -1;
-      for (int Wt = 1; Wt <= kQ4DecWarps; Wt *= 2) {
-        const int Wk = kQ4DecWarps / Wt;
-        const int64_t per = static_cast<int64_t>(clusters) * Wt;  // warp rows boxes in a round
-        const int64_t rounds = (N + 32 * per - 1) / (32 * per);
-        const int rw = static_cast<int>((N + per * rounds - 1) / (per * rounds));
-        const int TPW = rw > 16 ? 2 : 1, rows = 16 * TPW * Wt;
-        const int64_t nblocks = (N + static_cast<int64_t>(Wt) * rw - 1) / (static_cast<int64_t>(Wt) * rw);
-        const int64_t x = q4_dec_x_bytes(C, Gs) + q4_dec_f_bytes(C, Gs) + 8 * kQ4DecWarps * kQ4DecSlots;
-        const int64_t part = q4_dec_part_bytes(C, rows, Wk);
-        const int64_t fixed = 1024 + (nblocks <= clusters ? std::max(x, part) : x + part);
-        const int64_t left = budget - fixed;
-        const int slots = static_cast<int>(std::min<int64_t>(kQ4DecSlots, left / q4_dec_ring_bytes(TPW, 1)));
-        if (left <= 0 || slots < 2) continue;
-        const int64_t boxes = ((Gs + 1) / 2 + Wk - 1) / Wk;
-        const int64_t cost = rounds * (boxes * 2 * TPW + 2);
-        if (best >= 0 && cost >= best) continue;
-        best = cost;
-        const int64_t ring = q4_dec_ring_bytes(TPW, slots);
-        *out = Q4DecodePlan{NT, TPW, C, P, rw, static_cast<int>(nblocks), Wt, Wk, S, Gs, slots, clusters,
-                            static_cast<int>(nblocks <= clusters ? ring : ring + x),
-                            static_cast<size_t>(ring + fixed)};
-      }
-      if (best >= 0) return true;
-      if (G <= 2 * S) break;  // no finer split of K
+  int64_t best = -1;
+  for (int S = 1; S <= 2 && (S == 1 || G >= 8); ++S) {
+    const int Gs = ((G + S - 1) / S + 1) & ~1, clusters = std::max(1, sm_count / S);
+    const int64_t x = q4_dec_x_bytes(C, Gs) + q4_dec_f_bytes(C, Gs) + 8 * kQ4DecWarps * kQ4DecSlots;
+    const int64_t passes = (static_cast<int64_t>(M) * Gs + 8 * kQ4DecWarps - 1) / (8 * kQ4DecWarps);
+    for (int Wt = 1; Wt <= kQ4DecWarps; ++Wt) {
+      const int Wk = kQ4DecWarps / Wt;
+      const int64_t per = static_cast<int64_t>(clusters) * Wt;  // boxes of a round
+      const int64_t rounds = (N + kQ4DecBoxRows * per - 1) / (kQ4DecBoxRows * per);
+      const int rw = static_cast<int>((N + per * rounds - 1) / (per * rounds));
+      const int64_t nblocks = (N + static_cast<int64_t>(Wt) * rw - 1) / (static_cast<int64_t>(Wt) * rw);
+      const int64_t part = q4_dec_part_bytes(C, kQ4DecBoxRows * Wt, Wk);
+      const bool once = nblocks <= clusters;  // the partial sums then lie over x'
+      const int64_t smem = 1024 + kQ4DecRingBytes + (once ? std::max(x, part) : x + part);
+      if (smem > max_smem) continue;
+      const int64_t boxes = (Gs / 2 + Wk - 1) / Wk;
+      const int64_t cost =
+          rounds * (boxes * 2 * (300 + 200 * NT) + 3000 + (S > 1 ? 2500 : 0)) + passes * (copied ? 60 : 1200);
+      if (best >= 0 && cost >= best) continue;
+      best = cost;
+      *out = Q4DecodePlan{NT, C, P, rw, static_cast<int>(nblocks), Wt, Wk, S, Gs, clusters,
+                          static_cast<int>(once ? kQ4DecRingBytes : kQ4DecRingBytes + x), static_cast<size_t>(smem)};
     }
   }
-  return false;
+  return best >= 0;
 }
 
-template <int NT, int TPW>
+template <int NT>
 tb_status launch_q4_decode(const CUtensorMap& tm, const Q4DecodeParams& p, const Q4DecodePlan& pl, const DevInfo* d,
                            cudaStream_t st) {
-  auto k = q4_decode_kernel<NT, TPW>;
+  auto k = q4_decode_kernel<NT>;
   if (allow_smem(k, d) != TB_OK) return TB_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(pl.S * std::min(pl.clusters, pl.nblocks)));
@@ -1311,7 +1307,6 @@ tb_status run_q4_decode(const Q4Args& a, const DevInfo* d, const Q4DecodePlan& p
   p.Wk = pl.Wk;
   p.S = pl.S;
   p.Gs = pl.Gs;
-  p.slots = pl.slots;
   p.part_at = pl.part_at;
   CUtensorMap tm;
   if (make_map_2d(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.packed, a.K / 2, a.N, a.K / 2, 128,
@@ -1328,22 +1323,20 @@ tb_status run_q4_decode(const Q4Args& a, const DevInfo* d, const Q4DecodePlan& p
     p.x_scales = factors;
     p.xmode = Q4X_IMAGE;
   }
-#define TB_Q4D(NT) \
-  case NT: return pl.TPW == 2 ? launch_q4_decode<NT, 2>(tm, p, pl, d, a.st) : launch_q4_decode<NT, 1>(tm, p, pl, d, a.st);
   switch (pl.NT) {
-    TB_Q4D(1)
-    TB_Q4D(2)
-    TB_Q4D(3)
-    default: return pl.TPW == 2 ? launch_q4_decode<4, 2>(tm, p, pl, d, a.st) : launch_q4_decode<4, 1>(tm, p, pl, d, a.st);
+    case 1: return launch_q4_decode<1>(tm, p, pl, d, a.st);
+    case 2: return launch_q4_decode<2>(tm, p, pl, d, a.st);
+    case 3: return launch_q4_decode<3>(tm, p, pl, d, a.st);
+    default: return launch_q4_decode<4>(tm, p, pl, d, a.st);
   }
-#undef TB_Q4D
 }
 
 tb_status run_q4(const Q4Args& a, const DevInfo* d) {
   Q4DecodePlan pl;
   if (a.M <= kQ4DecMaxM) {
     const int P = q4_planes(a.xt == TB_INT8 ? Q4X_INT8 : Q4X_BF16, static_cast<int>(a.M));
-    if (q4_decode_plan(a.N, a.K, P * static_cast<int>(a.M), P, d->sm_count, d->max_smem_optin, &pl))
+    const bool copied = a.M > kQ4DecInCta || a.signs != nullptr;
+    if (q4_decode_plan(a.N, a.K, static_cast<int>(a.M), P, copied, d->sm_count, d->max_smem_optin, &pl))
       return run_q4_decode(a, d, pl);
   }
   return run_q4_gemm(a, d);

@@ -8,8 +8,8 @@ With T = sum |w| |x'|:
     off by less than 160 / 2 * 2^-24 T < 2^-17 T.
   * up to 16 tokens x' is held in 8-bit planes of a fixed-point number per
     128-group: one for an int8 (exact), three up to 5 tokens, else two.  The
-    largest of the group is at least 2^(8 P - 2) steps, so a value is off by half a
-    step, 2^-(8 P - 1) of the group's largest X: sum |w| X 2^-(8 P - 1) in all.
+    largest of the group, X, is at least 2^21 steps with three and 2^14 with two,
+    so a value is off by half a step, 2^-22 or 2^-15 of X: sum |w| X times that.
   * past 16 tokens a weight and, where x is rotated, x' are rounded to 11 bits:
     independent errors of 2^-11 / sqrt(3) rms each at most, so at most
     2^-11 sqrt(2/3) < 2^-11 of y in relative L2 over a whole output, and at most
@@ -176,7 +176,7 @@ class Linear:
         if self.m <= 16:
             top = np.repeat(xr.reshape(self.m, -1, 128).max(2), 128, axis=1)
             if self.xt != "int8":
-                tol += q4o.linear(top, np.abs(self.codes), self.scales, xs) * 2.0 ** (-23 if self.m <= 5 else -15)
+                tol += q4o.linear(top, np.abs(self.codes), self.scales, xs) * 2.0 ** (-22 if self.m <= 5 else -15)
             tol += big * (2.0 ** -17 if sg is None else 2.0 ** -10)
         else:
             tol += big * 2.0 ** -10
@@ -221,7 +221,7 @@ def within(y, x, w):
     tol = a @ w.abs().T * (2.0 ** -17 if m <= 16 else 2.0 ** -10)
     if m <= 16:
         top = a.view(m, -1, 128).amax(2).repeat_interleave(128, 1)
-        tol += top @ w.abs().T * 2.0 ** (-23 if m <= 5 else -15)
+        tol += top @ w.abs().T * 2.0 ** (-22 if m <= 5 else -15)
     return bool(((y.double() - x.double() @ w.T).abs() <= tol).all())
 
 
