@@ -5,7 +5,13 @@
 //   n_b <- H (d_b * n_b) / 32 per 1024-block (optional),
 //   y = n, or per group scale = max|n| / Q and y = round(n / scale).
 //
-// One block per row; the row is held in shared memory as fp32.
+// Bound by HBM past a few hundred rows, by the launch and two passes of latency
+// for one.  A row stays in registers between its one load and its one store: a
+// thread holds NV pieces of 8 values (16-byte loads of 16-bit types), a block a
+// row, and the blocks walk the rows.  In the rotated kernel a warp holds a whole
+// 1024-block, so the transform needs no block-wide barrier: distances 1-4, 256 and
+// 512 are in a lane, 8-128 after a transpose through 4 KB of shared memory and back
+// (128 wavefronts a block; 160 shuffles would be the other way).
 #pragma once
 #include <cuda_fp8.h>
 
@@ -14,8 +20,8 @@
 
 namespace tb {
 
-constexpr int kNormThreads = 256;
 constexpr int kNormMaxK = 32768;
+constexpr int kNormRotFloats = 4 * 264;  // a warp's transpose buffer: 8 floats of padding every 256
 
 // dtype codes of the C ABI as the kernels get them
 enum : int { DT_BF16 = 0, DT_FP16 = 1, DT_FP32 = 2, DT_INT8 = 3, DT_E4M3 = 5 };
@@ -36,6 +42,14 @@ __device__ __forceinline__ void store_from_f32(void* p, int64_t i, int dt, float
   }
 }
 
+__device__ __forceinline__ float round_to(float v, int dt) {
+  switch (dt) {
+    case DT_BF16: return __bfloat162float(__float2bfloat16_rn(v));
+    case DT_FP16: return __half2float(__float2half_rn(v));
+    default: return v;
+  }
+}
+
 // 8-bit code of v = n / scale
 __device__ __forceinline__ uint8_t code8(float v, int dt) {
   if (dt == DT_INT8) {
@@ -53,38 +67,52 @@ struct NormParams {
   const int8_t* signs;
   void* y;
   float* y_scales;
-  int64_t K;
+  int64_t M;
+  int K;
   int group;  // 0: floating output
   int xt, rt, wt, yt;
   float eps;
+  bool vec;  // every pointer allows 16-byte accesses (K % 8 == 0)
 };
 
-__device__ __forceinline__ float block_sum(float v, float* red) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float s = 0.f;
-  for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) s += red[w];
-  __syncthreads();
-  return s;
-}
-
 // Largest absolute value as its fp32 bits: NaN above infinity above the rest.
-__device__ __forceinline__ uint32_t block_max_bits(uint32_t v, uint32_t* red) {
-  v = __reduce_max_sync(0xffffffffu, v);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  uint32_t s = 0;
-  for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) s = max(s, red[w]);
-  __syncthreads();
-  return s;
-}
-
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
 constexpr uint32_t kInfBits = 0x7F800000u;
 constexpr uint32_t kTinyBits = (127u - 100u) << 23;  // 2^-100
+
+// Block-wide reductions with one barrier each: `red` holds two sets of 32 words
+// that consecutive reductions use in turn.
+struct BlockReduce {
+  uint32_t* red;
+  int set;
+  __device__ __forceinline__ uint32_t* next() {
+    set ^= 32;
+    return red + set;
+  }
+  __device__ __forceinline__ float sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    const int nw = blockDim.x >> 5, lane = threadIdx.x & 31;
+    if (nw == 1) return v;
+    uint32_t* r = next();
+    if (lane == 0) r[threadIdx.x >> 5] = __float_as_uint(v);
+    __syncthreads();
+    v = lane < nw ? __uint_as_float(r[lane]) : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  }
+  __device__ __forceinline__ uint32_t max_bits(uint32_t v) {
+    v = __reduce_max_sync(0xffffffffu, v);
+    const int nw = blockDim.x >> 5, lane = threadIdx.x & 31;
+    if (nw == 1) return v;
+    uint32_t* r = next();
+    if (lane == 0) r[threadIdx.x >> 5] = v;
+    __syncthreads();
+    return __reduce_max_sync(0xffffffffu, lane < nw ? r[lane] : 0u);
+  }
+};
 
 // Scale of a group with this largest |n| (as bits), and the factor that takes
 // n to n / scale.
@@ -100,86 +128,320 @@ __device__ __forceinline__ void group_scale(uint32_t amax_bits, float q, float* 
   }
 }
 
-__global__ void __launch_bounds__(kNormThreads) rms_norm_kernel(const NormParams p) {
-  extern __shared__ float row[];
-  __shared__ float red[kNormThreads / 32];
-  const int tid = threadIdx.x, K = static_cast<int>(p.K);
-  const int64_t base = static_cast<int64_t>(blockIdx.x) * p.K;
-  float ss = 0.f;
-  for (int k = tid; k < K; k += kNormThreads) {
-    float h = load_as_f32(p.x, base + k, p.xt);
-    if (p.residual != nullptr) {
-      h += load_as_f32(p.residual, base + k, p.rt);
-      store_from_f32(p.residual_out, base + k, p.rt, h);
-      h = load_as_f32(p.residual_out, base + k, p.rt);
+// 8 values at element i as they lie in memory: 16 or 32 bytes.
+__device__ __forceinline__ void norm_fetch8(const void* p, int64_t i, int dt, bool vec, uint4 (&u)[2]) {
+  if (vec) {
+    if (dt == DT_FP32) {
+      u[0] = *reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
+      u[1] = *reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i + 4);
+    } else {
+      u[0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
     }
-    row[k] = h;
-    ss += h * h;
+    return;
   }
-  ss = block_sum(ss, red);
-  float inv;
-  if (ss < 1e30f && ss > 1e-20f) {
-    inv = 1.f / sqrtf(ss / static_cast<float>(K) + p.eps);
+  if (dt == DT_FP32) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) (&u[e >> 2].x)[e & 3] = static_cast<const uint32_t*>(p)[i + e];
   } else {
-    // squares that leave fp32's range: sum them scaled by a power of two
-    uint32_t mb = 0;
-    for (int k = tid; k < K; k += kNormThreads) mb = max(mb, abs_bits(row[k]));
-    mb = block_max_bits(mb, reinterpret_cast<uint32_t*>(red));
-    const int e = mb >= kInfBits ? 0 : (mb == 0 ? 0 : ilogbf(__uint_as_float(mb)));
-    float s2 = 0.f;
-    for (int k = tid; k < K; k += kNormThreads) {
-      const float h = ldexpf(row[k], -e);
-      s2 += h * h;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      (&u[0].x)[e] = static_cast<const uint16_t*>(p)[i + 2 * e] |
+                     (static_cast<uint32_t>(static_cast<const uint16_t*>(p)[i + 2 * e + 1]) << 16);
+  }
+}
+
+__device__ __forceinline__ void norm_widen8(const uint4 (&u)[2], int dt, float (&v)[8]) {
+  if (dt == DT_FP32) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = __uint_as_float((&u[e >> 2].x)[e & 3]);
+  } else if (dt == DT_BF16) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[2 * e] = __uint_as_float((&u[0].x)[e] << 16);
+      v[2 * e + 1] = __uint_as_float((&u[0].x)[e] & 0xFFFF0000u);
     }
-    s2 = block_sum(s2, red);
-    inv = static_cast<float>(1.0 / sqrt(ldexp(static_cast<double>(s2) / K, 2 * e) + static_cast<double>(p.eps)));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&(&u[0].x)[e]));
+      v[2 * e] = f.x;
+      v[2 * e + 1] = f.y;
+    }
   }
-  for (int k = tid; k < K; k += kNormThreads) {
-    float n = row[k] * inv;
-    if (p.weight != nullptr) n *= load_as_f32(p.weight, k, p.wt);
-    if (p.signs != nullptr) n *= static_cast<float>(p.signs[k]);
-    row[k] = n;
+}
+
+__device__ __forceinline__ void norm_store8(void* p, int64_t i, int dt, bool vec, const float (&v)[8]) {
+  if (!vec) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) store_from_f32(p, i + e, dt, v[e]);
+  } else if (dt == DT_FP32) {
+    store8<float>(static_cast<float*>(p) + i, v);
+  } else if (dt == DT_BF16) {
+    store8<__nv_bfloat16>(static_cast<__nv_bfloat16*>(p) + i, v);
+  } else {
+    store8<__half>(static_cast<__half*>(p) + i, v);
   }
-  __syncthreads();
-  if (p.signs != nullptr) {
-    for (int h = 1; h < kHB; h <<= 1) {
-      for (int i = tid; i < K / 2; i += kNormThreads) {
-        const int a = 2 * (i & ~(h - 1)) + (i & (h - 1));
-        const float u = row[a], v = row[a + h];
-        row[a] = u + v;
-        row[a + h] = u - v;
+}
+
+// Codes of 8 values n with n / scale = n inv.
+__device__ __forceinline__ void norm_store_codes8(uint8_t* p, int64_t i, int dt, bool vec, const float (&v)[8],
+                                                  float inv) {
+  uint32_t w[2] = {0u, 0u};
+  if (dt == DT_INT8) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e >> 2] |= static_cast<uint32_t>(code8(v[e] * inv, DT_INT8)) << (8 * (e & 3));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      w[e >> 1] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(v[2 * e] * inv, v[2 * e + 1] * inv),
+                                                                  __NV_SATFINITE, __NV_E4M3))
+                   << (16 * (e & 1));
+  }
+  if (vec) {
+    *reinterpret_cast<uint2*>(p + i) = make_uint2(w[0], w[1]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p[i + e] = static_cast<uint8_t>(w[e >> 2] >> (8 * (e & 3)));
+  }
+}
+
+// Unnormalised transform of the warp's 1024 values: piece j of lane l holds
+// 256 j + 8 l .. + 7.  buf: kNormRotFloats floats of the warp's own.
+__device__ __forceinline__ void norm_fwht(float (&v)[4][8], float* buf, int lane) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int h = 1; h < 8; h <<= 1)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if ((i & h) == 0) {
+          const float a = v[j][i], b = v[j][i + h];
+          v[j][i] = a + b;
+          v[j][i + h] = a - b;
+        }
+#pragma unroll
+  for (int h = 1; h < 4; h <<= 1)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if ((j & h) == 0)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float a = v[j][i], b = v[j + h][i];
+          v[j][i] = a + b;
+          v[j + h][i] = a - b;
+        }
+  // transpose: lane 8 j + i takes the values 256 j + 8 l + i over l
+#pragma unroll
+  for (int j = 0; j < 4; ++j) store8<float>(buf + 264 * j + 8 * lane, v[j]);
+  __syncwarp();
+  float* col = buf + 264 * (lane >> 3) + (lane & 7);
+  float u[32];
+#pragma unroll
+  for (int l = 0; l < 32; ++l) u[l] = col[8 * l];
+#pragma unroll
+  for (int h = 1; h < 32; h <<= 1)
+#pragma unroll
+    for (int l = 0; l < 32; ++l)
+      if ((l & h) == 0) {
+        const float a = u[l], b = u[l + h];
+        u[l] = a + b;
+        u[l + h] = a - b;
       }
-      __syncthreads();
+#pragma unroll
+  for (int l = 0; l < 32; ++l) col[8 * l] = u[l];
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 4; ++j) load8<float>(buf + 264 * j + 8 * lane, v[j]);
+  __syncwarp();  // buf may be written again
+}
+
+// A piece is 8 consecutive values, piece j of thread t at 8 (j T + t) (rotated:
+// at 1024 warp + 256 j + 8 lane), or in the strided layout (K % 8 != 0) the
+// values (8 j + e) T + t, so that a warp's scalar accesses stay coalesced.
+enum : int { NORM_PIECES = 0, NORM_ROTATED = 1, NORM_STRIDED = 2 };
+
+template <int NV, int kMode, int kMaxThreads>
+__global__ void __launch_bounds__(kMaxThreads, 1) rms_norm_kernel(const NormParams p) {
+  extern __shared__ float norm_smem[];
+  __shared__ uint32_t red[64];
+  pdl_launch_dependents();
+  const int tid = threadIdx.x, T = blockDim.x, warp = tid >> 5, lane = tid & 31, K = p.K;
+  BlockReduce reduce{red, 0};
+  auto at = [&](int j) {
+    return kMode == NORM_ROTATED ? 1024 * warp + 256 * j + 8 * lane : (kMode == NORM_PIECES ? 8 * (j * T + tid) : 8 * j * T + tid);
+  };
+  pdl_wait();
+  for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x) {
+    const int64_t base = row * K;
+    float v[NV][8];
+    if constexpr (kMode == NORM_STRIDED) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int k = at(j) + e * T;
+          v[j][e] = k < K ? load_as_f32(p.x, base + k, p.xt) : 0.f;
+        }
+      if (p.residual != nullptr) {
+        float r[NV][8];
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int k = at(j) + e * T;
+            r[j][e] = k < K ? load_as_f32(p.residual, base + k, p.rt) : 0.f;
+          }
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int k = at(j) + e * T;
+            v[j][e] = round_to(v[j][e] + r[j][e], p.rt);
+            if (k < K) store_from_f32(p.residual_out, base + k, p.rt, v[j][e]);
+          }
+      }
+    } else {
+      uint4 xu[NV][2] = {};
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (at(j) < K) norm_fetch8(p.x, base + at(j), p.xt, p.vec, xu[j]);
+      if (p.residual != nullptr) {
+        uint4 ru[NV][2] = {};
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+          if (at(j) < K) norm_fetch8(p.residual, base + at(j), p.rt, p.vec, ru[j]);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          float r[8];
+          norm_widen8(xu[j], p.xt, v[j]);
+          norm_widen8(ru[j], p.rt, r);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[j][e] = round_to(v[j][e] + r[e], p.rt);
+          if (at(j) < K) norm_store8(p.residual_out, base + at(j), p.rt, p.vec, v[j]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) norm_widen8(xu[j], p.xt, v[j]);
+      }
     }
-    for (int k = tid; k < K; k += kNormThreads) row[k] *= kHNorm;
-    __syncthreads();
-  }
-  if (p.group == 0) {
-    for (int k = tid; k < K; k += kNormThreads) store_from_f32(p.y, base + k, p.yt, row[k]);
-    return;
-  }
-  const float q = p.yt == DT_INT8 ? 127.f : 448.f;
-  uint8_t* y = static_cast<uint8_t*>(p.y);
-  if (p.group == K) {
-    uint32_t mb = 0;
-    for (int k = tid; k < K; k += kNormThreads) mb = max(mb, abs_bits(row[k]));
-    mb = block_max_bits(mb, reinterpret_cast<uint32_t*>(red));
+    float ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(v[j][e], v[j][e], ss);
+    ss = reduce.sum(ss);
+    float inv;
+    if (ss < 1e30f && ss > 1e-20f) {
+      inv = 1.f / sqrtf(ss / static_cast<float>(K) + p.eps);
+    } else {
+      // squares that leave fp32's range: sum them scaled by a power of two
+      uint32_t mb = 0;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mb = max(mb, abs_bits(v[j][e]));
+      mb = reduce.max_bits(mb);
+      const int ex = mb >= kInfBits ? 0 : (mb == 0 ? 0 : ilogbf(__uint_as_float(mb)));
+      float s2 = 0.f;
+      for (int j = 0; j < NV; ++j)
+        for (int e = 0; e < 8; ++e) {
+          const float h = ldexpf(v[j][e], -ex);
+          s2 += h * h;
+        }
+      s2 = reduce.sum(s2);
+      inv = static_cast<float>(1.0 / sqrt(ldexp(static_cast<double>(s2) / K, 2 * ex) + static_cast<double>(p.eps)));
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[j][e] *= inv;
+      if (p.weight != nullptr) {
+        if constexpr (kMode == NORM_STRIDED) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int k = at(j) + e * T;
+            if (k < K) v[j][e] *= load_as_f32(p.weight, k, p.wt);
+          }
+        } else if (at(j) < K) {
+          uint4 wu[2] = {};
+          float w[8];
+          norm_fetch8(p.weight, at(j), p.wt, p.vec, wu);
+          norm_widen8(wu, p.wt, w);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[j][e] *= w[e];
+        }
+      }
+    }
+    if constexpr (kMode == NORM_ROTATED) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        float d[8];
+        load_signs8(p.signs + at(j), d);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[j][e] *= d[e];
+      }
+      norm_fwht(v, norm_smem + warp * kNormRotFloats, lane);
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[j][e] *= kHNorm;
+    }
+    if (p.group == 0) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        if constexpr (kMode == NORM_STRIDED) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int k = at(j) + e * T;
+            if (k < K) store_from_f32(p.y, base + k, p.yt, v[j][e]);
+          }
+        } else if (at(j) < K) {
+          norm_store8(p.y, base + at(j), p.yt, p.vec, v[j]);
+        }
+      }
+      continue;
+    }
+    const float q = p.yt == DT_INT8 ? 127.f : 448.f;
+    uint8_t* y = static_cast<uint8_t*>(p.y);
+    uint32_t mb[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      mb[j] = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) mb[j] = max(mb[j], abs_bits(v[j][e]));
+    }
     float scale, is;
-    group_scale(mb, q, &scale, &is);
-    if (tid == 0) p.y_scales[blockIdx.x] = scale;
-    for (int k = tid; k < K; k += kNormThreads) y[base + k] = code8(row[k] * is, p.yt);
-    return;
-  }
-  // groups of 128: one warp each, in turn
-  const int warp = tid >> 5, lane = tid & 31, G = K / 128;
-  for (int g = warp; g < G; g += kNormThreads / 32) {
-    uint32_t mb = 0;
-    for (int j = lane; j < 128; j += 32) mb = max(mb, abs_bits(row[128 * g + j]));
-    mb = __reduce_max_sync(0xffffffffu, mb);
-    float scale, is;
-    group_scale(mb, q, &scale, &is);
-    if (lane == 0) p.y_scales[static_cast<int64_t>(blockIdx.x) * G + g] = scale;
-    for (int j = lane; j < 128; j += 32) y[base + 128 * g + j] = code8(row[128 * g + j] * is, p.yt);
+    if (p.group == K) {
+#pragma unroll
+      for (int j = 1; j < NV; ++j) mb[0] = max(mb[0], mb[j]);
+      group_scale(reduce.max_bits(mb[0]), q, &scale, &is);
+      if (tid == 0) p.y_scales[row] = scale;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        if constexpr (kMode == NORM_STRIDED) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int k = at(j) + e * T;
+            if (k < K) y[base + k] = code8(v[j][e] * is, p.yt);
+          }
+        } else if (at(j) < K) {
+          norm_store_codes8(y, base + at(j), p.yt, p.vec, v[j], is);
+        }
+      }
+    } else if constexpr (kMode != NORM_STRIDED) {
+      // groups of 128: 16 lanes of a piece
+      const int64_t G = K / 128;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) mb[j] = max(mb[j], __shfl_xor_sync(0xffffffffu, mb[j], o));
+        group_scale(mb[j], q, &scale, &is);
+        if (at(j) < K) {
+          if ((lane & 15) == 0) p.y_scales[row * G + (at(j) >> 7)] = scale;
+          norm_store_codes8(y, base + at(j), p.yt, p.vec, v[j], is);
+        }
+      }
+    }
   }
 }
 

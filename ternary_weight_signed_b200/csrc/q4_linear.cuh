@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(kHThreads)
                    const int8_t* __restrict__ signs, __half* __restrict__ out, float* __restrict__ factor, int K) {
   constexpr bool k8 = sizeof(TIn) == 1;
   __shared__ float sm[kHB];
-  __shared__ uint32_t red[kHThreads / 32];
+  __shared__ uint32_t red[64];
   pdl_launch_dependents();
   const int64_t row = blockIdx.x;
   const int tid = threadIdx.x, G = K / 128;
@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kHThreads)
         for (int i = 0; i < 8; ++i) mb = max(mb, abs_bits(v[i]));
       }
     }
-    mb = block_max_bits(mb, red);
+    mb = BlockReduce{red, 0}.max_bits(mb);
     // 2^e <= largest < 2^(e+1); a row that holds a NaN or an infinity stays as it is
     const int top = signs != nullptr ? 9 : 14;
     const int e = mb >= kInfBits ? 0 : max(static_cast<int>(mb >> 23) - 127, -96) - top;

@@ -1102,6 +1102,44 @@ tb_status linear_impl(const LinearArgs& a, int path) {
   }
 }
 
+// ------------------------------------------------------------------ RMS norm
+template <int NV, int kMode, int kMaxThreads>
+tb_status launch_norm(const NormParams& p, const DevInfo* d, int threads, size_t smem, cudaStream_t st) {
+  auto k = rms_norm_kernel<NV, kMode, kMaxThreads>;
+  if (smem > 0 && allow_smem(k, d) != TB_OK) return TB_ERR_CUDA;
+  // the blocks that fit the SMs (2048 threads each) walk the rows
+  const int64_t blocks = static_cast<int64_t>(d->sm_count) * std::min(32, 2048 / threads);
+  return launch_pdl(k, dim3(static_cast<unsigned>(std::min(p.M, blocks))), dim3(static_cast<unsigned>(threads)), smem, st,
+                    p);
+}
+
+template <int kMode>
+tb_status run_norm_pieces(const NormParams& p, const DevInfo* d, cudaStream_t st) {
+  // pieces of a thread: one where a row is alone on its SM (latency), else up to
+  // four (more bytes in flight a thread, fewer barriers a byte)
+  const int pieces = (p.K + 7) / 8;
+  int nv = 1;
+  while (nv < 4 && (pieces > 1024 * nv || (p.M > 2 * d->sm_count && pieces >= 256 * nv))) nv *= 2;
+  const int threads = ((pieces + nv - 1) / nv + 31) / 32 * 32;
+  switch (nv) {
+    case 1: return launch_norm<1, kMode, 1024>(p, d, threads, 0, st);
+    case 2: return launch_norm<2, kMode, 1024>(p, d, threads, 0, st);
+    default:
+      return threads <= 512 ? launch_norm<4, kMode, 512>(p, d, threads, 0, st)
+                            : launch_norm<4, kMode, 1024>(p, d, threads, 0, st);
+  }
+}
+
+tb_status run_norm(const NormParams& p, const DevInfo* d, cudaStream_t st) {
+  if (p.signs != nullptr) {
+    const int warps = p.K / kHB;
+    const size_t smem = sizeof(float) * kNormRotFloats * warps;
+    return warps <= 16 ? launch_norm<4, NORM_ROTATED, 512>(p, d, 32 * warps, smem, st)
+                       : launch_norm<4, NORM_ROTATED, 1024>(p, d, 32 * warps, smem, st);
+  }
+  return p.K % 8 == 0 ? run_norm_pieces<NORM_PIECES>(p, d, st) : run_norm_pieces<NORM_STRIDED>(p, d, st);
+}
+
 // ------------------------------------------------------------------ 4-bit linear
 struct Q4Args {
   const void* x;
@@ -1603,11 +1641,12 @@ tb_status tb_rms_norm(const void* x, tb_dtype xt, const void* residual, void* re
   const DevInfo* d = nullptr;
   const tb_status st = current_device(&d);
   if (st != TB_OK) return st;
-  NormParams p{x, residual, residual_out, weight, signs, y, y_scales, K, static_cast<int>(scale_group),
-               xt, rt, wt, yt, eps};
-  if (allow_smem(rms_norm_kernel, d) != TB_OK) return TB_ERR_CUDA;
-  rms_norm_kernel<<<static_cast<unsigned>(M), kNormThreads, static_cast<size_t>(4 * K), as_stream(stream)>>>(p);
-  return launch_status();
+  const bool vec = K % 8 == 0 && aligned(x, 16) && aligned(y, y8 ? 8 : 16) &&
+                   (residual == nullptr || (aligned(residual, 16) && aligned(residual_out, 16))) &&
+                   (weight == nullptr || aligned(weight, 16));
+  const NormParams p{x, residual, residual_out, weight, signs, y, y_scales, M, static_cast<int>(K),
+                     static_cast<int>(scale_group), xt, rt, wt, yt, eps, vec};
+  return run_norm(p, d, as_stream(stream));
 }
 
 size_t tb_q4_packed_bytes(int64_t N, int64_t K) {
