@@ -170,6 +170,39 @@ __device__ __forceinline__ void norm_widen8(const uint4 (&u)[2], int dt, float (
   }
 }
 
+// v rounded to dt and stored at element i (when `in`); v keeps the rounded values.
+__device__ __forceinline__ void norm_round_store8(void* p, int64_t i, int dt, bool vec, bool in, float (&v)[8]) {
+  uint4 u[2] = {};
+  if (dt == DT_FP32) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) (&u[e >> 2].x)[e & 3] = __float_as_uint(v[e]);
+  } else if (dt == DT_BF16) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+      (&u[0].x)[e] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const __half2 b = __floats2half2_rn(v[2 * e], v[2 * e + 1]);
+      (&u[0].x)[e] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+  }
+  norm_widen8(u, dt, v);
+  if (!in) return;
+  if (!vec) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) store_from_f32(p, i + e, dt, v[e]);  // exact
+  } else if (dt == DT_FP32) {
+    uint4* q = reinterpret_cast<uint4*>(static_cast<float*>(p) + i);
+    q[0] = u[0];
+    q[1] = u[1];
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = u[0];
+  }
+}
+
 __device__ __forceinline__ void norm_store8(void* p, int64_t i, int dt, bool vec, const float (&v)[8]) {
   if (!vec) {
 #pragma unroll
@@ -205,72 +238,143 @@ __device__ __forceinline__ void norm_store_codes8(uint8_t* p, int64_t i, int dt,
   }
 }
 
+// Two butterflies at once: (a, b) <- (a + b, a - b) on pairs of floats (packed
+// fp32 adds; a - b as a + b (-1), the same rounding).
+__device__ __forceinline__ void butterfly2(float2& a, float2& b) {
+  const unsigned long long minus = 0xBF800000BF800000ull;
+  unsigned long long s, d;
+  const unsigned long long x = *reinterpret_cast<unsigned long long*>(&a), y = *reinterpret_cast<unsigned long long*>(&b);
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(s) : "l"(x), "l"(y));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(y), "l"(minus), "l"(x));
+  a = *reinterpret_cast<float2*>(&s);
+  b = *reinterpret_cast<float2*>(&d);
+}
+
+// Transform of 32 values (16 pairs) over all five index bits.
+__device__ __forceinline__ void norm_fwht32(float2 (&u)[16]) {
+#pragma unroll
+  for (int l = 0; l < 16; ++l) u[l] = make_float2(u[l].x + u[l].y, u[l].x - u[l].y);
+#pragma unroll
+  for (int h = 1; h < 16; h <<= 1)
+#pragma unroll
+    for (int l = 0; l < 16; ++l)
+      if ((l & h) == 0) butterfly2(u[l], u[l + h]);
+}
+
 // Unnormalised transform of the warp's 1024 values: piece j of lane l holds
 // 256 j + 8 l .. + 7.  buf: kNormRotFloats floats of the warp's own.
 __device__ __forceinline__ void norm_fwht(float (&v)[4][8], float* buf, int lane) {
+  float2 u[16];
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-#pragma unroll
-    for (int h = 1; h < 8; h <<= 1)
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if ((i & h) == 0) {
-          const float a = v[j][i], b = v[j][i + h];
-          v[j][i] = a + b;
-          v[j][i + h] = a - b;
-        }
-#pragma unroll
-  for (int h = 1; h < 4; h <<= 1)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if ((j & h) == 0)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float a = v[j][i], b = v[j + h][i];
-          v[j][i] = a + b;
-          v[j + h][i] = a - b;
-        }
+  for (int l = 0; l < 16; ++l) u[l] = make_float2(v[l >> 2][2 * (l & 3)], v[l >> 2][2 * (l & 3) + 1]);
+  norm_fwht32(u);  // over e and j
   // transpose: lane 8 j + i takes the values 256 j + 8 l + i over l
 #pragma unroll
-  for (int j = 0; j < 4; ++j) store8<float>(buf + 264 * j + 8 * lane, v[j]);
+  for (int l = 0; l < 16; l += 2)
+    *reinterpret_cast<float4*>(buf + 264 * (l >> 2) + 8 * lane + 2 * (l & 3)) =
+        make_float4(u[l].x, u[l].y, u[l + 1].x, u[l + 1].y);
   __syncwarp();
   float* col = buf + 264 * (lane >> 3) + (lane & 7);
-  float u[32];
 #pragma unroll
-  for (int l = 0; l < 32; ++l) u[l] = col[8 * l];
+  for (int l = 0; l < 16; ++l) u[l] = make_float2(col[16 * l], col[16 * l + 8]);
+  norm_fwht32(u);  // over the lane
 #pragma unroll
-  for (int h = 1; h < 32; h <<= 1)
-#pragma unroll
-    for (int l = 0; l < 32; ++l)
-      if ((l & h) == 0) {
-        const float a = u[l], b = u[l + h];
-        u[l] = a + b;
-        u[l + h] = a - b;
-      }
-#pragma unroll
-  for (int l = 0; l < 32; ++l) col[8 * l] = u[l];
+  for (int l = 0; l < 16; ++l) {
+    col[16 * l] = u[l].x;
+    col[16 * l + 8] = u[l].y;
+  }
   __syncwarp();
 #pragma unroll
   for (int j = 0; j < 4; ++j) load8<float>(buf + 264 * j + 8 * lane, v[j]);
   __syncwarp();  // buf may be written again
 }
 
-// A piece is 8 consecutive values, piece j of thread t at 8 (j T + t) (rotated:
-// at 1024 warp + 256 j + 8 lane), or in the strided layout (K % 8 != 0) the
-// values (8 j + e) T + t, so that a warp's scalar accesses stay coalesced.
+// Layouts of a row over the threads: a piece is 8 consecutive values, piece j of
+// thread t at 8 (j T + t) (rotated: at 1024 warp + 256 j + 8 lane); strided
+// (K % 8 != 0): the values (8 j + e) T + t, so that a warp's scalar accesses stay
+// coalesced.
 enum : int { NORM_PIECES = 0, NORM_ROTATED = 1, NORM_STRIDED = 2 };
 
-template <int NV, int kMode, int kMaxThreads>
+// The weights from element k on as they lie in memory (ones when there are none),
+// in the rotated kernel with the signs on them.
+template <int kMode>
+__device__ __forceinline__ void norm_weight8(const NormParams& p, int k, uint4 (&u)[2]) {
+  if (p.weight != nullptr) {
+    norm_fetch8(p.weight, k, p.wt, p.vec, u);
+  } else {
+    const uint32_t one = p.wt == DT_FP32 ? 0x3F800000u : (p.wt == DT_BF16 ? 0x3F803F80u : 0x3C003C00u);
+    u[0] = u[1] = make_uint4(one, one, one, one);
+  }
+  if constexpr (kMode == NORM_ROTATED) {
+    const uint2 s = *reinterpret_cast<const uint2*>(p.signs + k);
+    if (p.wt == DT_FP32) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) (&u[e >> 2].x)[e & 3] ^= ((e < 4 ? s.x : s.y) << (24 - 8 * (e & 3))) & 0x80000000u;
+    } else {
+      // signs (e, e + 1) in the top bits of the halves
+#pragma unroll
+      for (int e = 0; e < 4; ++e) (&u[0].x)[e] ^= __byte_perm(e < 2 ? s.x : s.y, 0u, (e & 1) ? 0x3424u : 0x1404u) & 0x80008000u;
+    }
+  }
+}
+
+// kBulk: the rows come through shared memory, each by one or two bulk copies
+// issued kNormStages rows ahead (one is enough beside three to six blocks on an
+// SM; two leave room for fewer blocks: 170 against 149 us for 16384 x 5120), so that the copies of the next rows run while a
+// row is reduced, rotated and stored, and the weights (with the signs) lie there
+// too; for many rows (16-byte accesses only).
+constexpr int kNormStages = 1;
+
+template <int NV, int kMode, int kMaxThreads, bool kBulk>
 __global__ void __launch_bounds__(kMaxThreads, 1) rms_norm_kernel(const NormParams p) {
-  extern __shared__ float norm_smem[];
+  extern __shared__ __align__(16) float norm_smem[];
   __shared__ uint32_t red[64];
+  __shared__ uint64_t bars[kNormStages];
   pdl_launch_dependents();
   const int tid = threadIdx.x, T = blockDim.x, warp = tid >> 5, lane = tid & 31, K = p.K;
   BlockReduce reduce{red, 0};
   auto at = [&](int j) {
     return kMode == NORM_ROTATED ? 1024 * warp + 256 * j + 8 * lane : (kMode == NORM_PIECES ? 8 * (j * T + tid) : 8 * j * T + tid);
   };
+  uint8_t* weights = reinterpret_cast<uint8_t*>(norm_smem + (kMode == NORM_ROTATED ? (T >> 5) * kNormRotFloats : 0));
+  const int w_size = p.wt == DT_FP32 ? 4 : 2;
+  uint8_t* stages = weights + K * w_size;
+  const uint32_t x_bytes = static_cast<uint32_t>(K) * (p.xt == DT_FP32 ? 4 : 2);
+  const uint32_t r_bytes = p.residual == nullptr ? 0u : static_cast<uint32_t>(K) * (p.rt == DT_FP32 ? 4 : 2);
+  auto fetch = [&](int64_t row, int s) {
+    uint8_t* dst = stages + s * (x_bytes + r_bytes);
+    mbar_arrive_expect_tx(&bars[s], x_bytes + r_bytes);
+    bulk_load(dst, static_cast<const uint8_t*>(p.x) + row * x_bytes, x_bytes, &bars[s]);
+    if (r_bytes != 0) bulk_load(dst + x_bytes, static_cast<const uint8_t*>(p.residual) + row * r_bytes, r_bytes, &bars[s]);
+  };
+  if constexpr (kBulk) {
+    if (tid == 0) {
+      for (int s = 0; s < kNormStages; ++s) mbar_init(&bars[s], 1);
+      fence_mbar_init();
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (at(j) < K) {
+        uint4 w[2];
+        norm_weight8<kMode>(p, at(j), w);
+        uint4* dst = reinterpret_cast<uint4*>(weights + at(j) * w_size);
+        dst[0] = w[0];
+        if (w_size == 4) dst[1] = w[1];
+      }
+    __syncthreads();
+  }
   pdl_wait();
+  if constexpr (kBulk) {
+    if (tid == 0) {
+      for (int s = 0; s < kNormStages; ++s) {
+        const int64_t row = blockIdx.x + static_cast<int64_t>(s) * gridDim.x;
+        if (row < p.M) fetch(row, s);
+      }
+    }
+  }
+  bool ok = true;
+  int stage = 0;
+  uint32_t phase = 0;
   for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x) {
     const int64_t base = row * K;
     float v[NV][8];
@@ -301,27 +405,49 @@ __global__ void __launch_bounds__(kMaxThreads, 1) rms_norm_kernel(const NormPara
           }
       }
     } else {
-      uint4 xu[NV][2] = {};
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-        if (at(j) < K) norm_fetch8(p.x, base + at(j), p.xt, p.vec, xu[j]);
-      if (p.residual != nullptr) {
-        uint4 ru[NV][2] = {};
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-          if (at(j) < K) norm_fetch8(p.residual, base + at(j), p.rt, p.vec, ru[j]);
+      if constexpr (kBulk) {
+        // after a wait that gave up the rows are wrong and the fault word says so
+        ok = ok && mbar_wait(&bars[stage], phase, FAULT_WAIT_FULL);
+        const uint8_t* st = stages + stage * (x_bytes + r_bytes);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-          float r[8];
-          norm_widen8(xu[j], p.xt, v[j]);
-          norm_widen8(ru[j], p.rt, r);
+          uint4 u[2] = {};
+          if (at(j) < K) norm_fetch8(st, at(j), p.xt, true, u);
+          norm_widen8(u, p.xt, v[j]);
+          if (r_bytes != 0) {
+            uint4 w[2] = {};
+            float r[8];
+            if (at(j) < K) norm_fetch8(st + x_bytes, at(j), p.rt, true, w);
+            norm_widen8(w, p.rt, r);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[j][e] = round_to(v[j][e] + r[e], p.rt);
-          if (at(j) < K) norm_store8(p.residual_out, base + at(j), p.rt, p.vec, v[j]);
+            for (int e = 0; e < 8; ++e) v[j][e] += r[e];
+            norm_round_store8(p.residual_out, base + at(j), p.rt, true, at(j) < K, v[j]);
+          }
         }
       } else {
+        // all loads before the first store
+        uint4 xu[NV][2] = {};
 #pragma unroll
-        for (int j = 0; j < NV; ++j) norm_widen8(xu[j], p.xt, v[j]);
+        for (int j = 0; j < NV; ++j)
+          if (at(j) < K) norm_fetch8(p.x, base + at(j), p.xt, p.vec, xu[j]);
+        if (p.residual != nullptr) {
+          uint4 ru[NV][2] = {};
+#pragma unroll
+          for (int j = 0; j < NV; ++j)
+            if (at(j) < K) norm_fetch8(p.residual, base + at(j), p.rt, p.vec, ru[j]);
+#pragma unroll
+          for (int j = 0; j < NV; ++j) {
+            float r[8];
+            norm_widen8(xu[j], p.xt, v[j]);
+            norm_widen8(ru[j], p.rt, r);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[j][e] += r[e];
+            norm_round_store8(p.residual_out, base + at(j), p.rt, p.vec, at(j) < K, v[j]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < NV; ++j) norm_widen8(xu[j], p.xt, v[j]);
+        }
       }
     }
     float ss = 0.f;
@@ -330,6 +456,15 @@ __global__ void __launch_bounds__(kMaxThreads, 1) rms_norm_kernel(const NormPara
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = fmaf(v[j][e], v[j][e], ss);
     ss = reduce.sum(ss);
+    if constexpr (kBulk) {
+      // every thread has its values in registers: the stage takes a later row
+      if (tid == 0 && row + static_cast<int64_t>(kNormStages) * gridDim.x < p.M)
+        fetch(row + static_cast<int64_t>(kNormStages) * gridDim.x, stage);
+      if (++stage == kNormStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
     float inv;
     if (ss < 1e30f && ss > 1e-20f) {
       inv = 1.f / sqrtf(ss / static_cast<float>(K) + p.eps);
@@ -351,41 +486,32 @@ __global__ void __launch_bounds__(kMaxThreads, 1) rms_norm_kernel(const NormPara
       s2 = reduce.sum(s2);
       inv = static_cast<float>(1.0 / sqrt(ldexp(static_cast<double>(s2) / K, 2 * ex) + static_cast<double>(p.eps)));
     }
+    if constexpr (kMode == NORM_ROTATED) inv *= kHNorm;  // the transform's 1/32
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[j][e] *= inv;
-      if (p.weight != nullptr) {
-        if constexpr (kMode == NORM_STRIDED) {
+      if constexpr (kMode == NORM_STRIDED) {
+        if (p.weight != nullptr) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const int k = at(j) + e * T;
             if (k < K) v[j][e] *= load_as_f32(p.weight, k, p.wt);
           }
-        } else if (at(j) < K) {
-          uint4 wu[2] = {};
-          float w[8];
-          norm_fetch8(p.weight, at(j), p.wt, p.vec, wu);
-          norm_widen8(wu, p.wt, w);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[j][e] *= w[e];
         }
+      } else if (at(j) < K) {
+        uint4 u[2] = {};
+        float w[8];
+        if constexpr (kBulk)
+          norm_fetch8(weights, at(j), p.wt, true, u);
+        else
+          norm_weight8<kMode>(p, at(j), u);
+        norm_widen8(u, p.wt, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[j][e] *= w[e];
       }
     }
-    if constexpr (kMode == NORM_ROTATED) {
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        float d[8];
-        load_signs8(p.signs + at(j), d);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[j][e] *= d[e];
-      }
-      norm_fwht(v, norm_smem + warp * kNormRotFloats, lane);
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[j][e] *= kHNorm;
-    }
+    if constexpr (kMode == NORM_ROTATED) norm_fwht(v, norm_smem + warp * kNormRotFloats, lane);
     if (p.group == 0) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {

@@ -1103,14 +1103,31 @@ tb_status linear_impl(const LinearArgs& a, int path) {
 }
 
 // ------------------------------------------------------------------ RMS norm
-template <int NV, int kMode, int kMaxThreads>
+template <int NV, int kMode, int kMaxThreads, bool kBulk = false>
 tb_status launch_norm(const NormParams& p, const DevInfo* d, int threads, size_t smem, cudaStream_t st) {
-  auto k = rms_norm_kernel<NV, kMode, kMaxThreads>;
+  auto k = rms_norm_kernel<NV, kMode, kMaxThreads, kBulk>;
   if (smem > 0 && allow_smem(k, d) != TB_OK) return TB_ERR_CUDA;
-  // the blocks that fit the SMs (2048 threads each) walk the rows
-  const int64_t blocks = static_cast<int64_t>(d->sm_count) * std::min(32, 2048 / threads);
+  // as many blocks as fit the SMs walk the rows
+  int per_sm = std::min(32, 2048 / threads);
+  if (kBulk) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, threads, smem) != cudaSuccess || per_sm < 1) {
+      cudaGetLastError();
+      return TB_ERR_CUDA;
+    }
+  }
+  const int64_t blocks = static_cast<int64_t>(d->sm_count) * per_sm;
   return launch_pdl(k, dim3(static_cast<unsigned>(std::min(p.M, blocks))), dim3(static_cast<unsigned>(threads)), smem, st,
                     p);
+}
+
+// Bulk copies ahead pay from a few rows a block on, when a row is worth a copy.
+bool norm_bulk(const NormParams& p, const DevInfo* d, size_t smem) {
+  return p.vec && p.K >= 1024 && p.M >= 8 * d->sm_count && 2 * (smem + 2048) <= static_cast<size_t>(d->max_smem_optin);
+}
+
+size_t norm_stage_bytes(const NormParams& p) {
+  return (p.wt == TB_FP32 ? 4 : 2) * static_cast<size_t>(p.K) + kNormStages * static_cast<size_t>(p.K) *
+         ((p.xt == TB_FP32 ? 4 : 2) + (p.residual == nullptr ? 0 : (p.rt == TB_FP32 ? 4 : 2)));
 }
 
 template <int kMode>
@@ -1121,6 +1138,16 @@ tb_status run_norm_pieces(const NormParams& p, const DevInfo* d, cudaStream_t st
   int nv = 1;
   while (nv < 4 && (pieces > 1024 * nv || (p.M > 2 * d->sm_count && pieces >= 256 * nv))) nv *= 2;
   const int threads = ((pieces + nv - 1) / nv + 31) / 32 * 32;
+  if constexpr (kMode == NORM_PIECES) {
+    const size_t smem = norm_stage_bytes(p);
+    if (threads <= 512 && norm_bulk(p, d, smem)) {
+      switch (nv) {
+        case 1: return launch_norm<1, kMode, 512, true>(p, d, threads, smem, st);
+        case 2: return launch_norm<2, kMode, 512, true>(p, d, threads, smem, st);
+        default: return launch_norm<4, kMode, 512, true>(p, d, threads, smem, st);
+      }
+    }
+  }
   switch (nv) {
     case 1: return launch_norm<1, kMode, 1024>(p, d, threads, 0, st);
     case 2: return launch_norm<2, kMode, 1024>(p, d, threads, 0, st);
@@ -1134,8 +1161,10 @@ tb_status run_norm(const NormParams& p, const DevInfo* d, cudaStream_t st) {
   if (p.signs != nullptr) {
     const int warps = p.K / kHB;
     const size_t smem = sizeof(float) * kNormRotFloats * warps;
-    return warps <= 16 ? launch_norm<4, NORM_ROTATED, 512>(p, d, 32 * warps, smem, st)
-                       : launch_norm<4, NORM_ROTATED, 1024>(p, d, 32 * warps, smem, st);
+    if (warps > 16) return launch_norm<4, NORM_ROTATED, 1024>(p, d, 32 * warps, smem, st);
+    if (norm_bulk(p, d, smem + norm_stage_bytes(p)))
+      return launch_norm<4, NORM_ROTATED, 512, true>(p, d, 32 * warps, smem + norm_stage_bytes(p), st);
+    return launch_norm<4, NORM_ROTATED, 512>(p, d, 32 * warps, smem, st);
   }
   return p.K % 8 == 0 ? run_norm_pieces<NORM_PIECES>(p, d, st) : run_norm_pieces<NORM_STRIDED>(p, d, st);
 }
@@ -1645,7 +1674,7 @@ tb_status tb_rms_norm(const void* x, tb_dtype xt, const void* residual, void* re
                    (residual == nullptr || (aligned(residual, 16) && aligned(residual_out, 16))) &&
                    (weight == nullptr || aligned(weight, 16));
   const NormParams p{x, residual, residual_out, weight, signs, y, y_scales, M, static_cast<int>(K),
-                     static_cast<int>(scale_group), xt, rt, wt, yt, eps, vec};
+                     static_cast<int>(scale_group), xt, rt, weight == nullptr ? TB_BF16 : wt, yt, eps, vec};
   return run_norm(p, d, as_stream(stream));
 }
 

@@ -142,6 +142,27 @@ def test_eight_bits(yt, m, k, grouped, signs, xt, rt):
     Norm(k + m, m, k, xt, rt, "fp16", signs, yt, 128 if grouped else k).run().check()
 
 
+@pytest.mark.parametrize("m,k,xt,rt,signs,yt,grouped", [
+    (1300, 1024, "bf16", "bf16", True, "int8", True), (1190, 1032, "fp16", "fp32", False, "bf16", False),
+    (2600, 1024, "fp32", None, False, "fp16", False), (1200, 5120, "bf16", "fp32", False, "e4m3", True),
+    (1184, 5120, "bf16", "bf16", True, "bf16", False), (1185, 2048, "fp16", None, True, "e4m3", False),
+    (1400, 2560, "bf16", "bf16", False, "int8", False), (1201, 13312, "bf16", None, False, "int8", True),
+    (3000, 1000, "fp16", "bf16", False, "bf16", False)])
+def test_many_rows(m, k, xt, rt, signs, yt, grouped):
+    """Rows that come by copies issued ahead, several a block (and a width just under)."""
+    group = 0 if yt not in TOP else (128 if grouped else k)
+    c = Norm(k + m, m, k, xt, rt, "bf16", signs, yt, group).run(guard=1)
+    c.check()
+    # in place over the residual, and y over x where the types allow it
+    if rt:
+        r = c.dr.clone()
+        y = c.dx.clone() if xt == yt else torch.empty_like(c.y[:m * k])
+        x = y if xt == yt else c.dx
+        s = torch.empty(m, k // group, device=DEV) if group else None
+        tb.tb_rms_norm(x, T[xt][0], r, r, T[rt][0], c.dw, tb.TB_BF16, EPS, c.ds, m, k, y, T[yt][0], s, group)
+        assert torch.equal(r, c.ro) and torch.equal(y.view(-1).view(torch.uint8), c.y[:m * k].view(torch.uint8))
+
+
 @pytest.mark.parametrize("yt,group", [("bf16", 0), ("int8", 128), ("e4m3", 1024)])
 @pytest.mark.parametrize("signs", [False, True])
 def test_unaligned_and_no_weight(yt, group, signs):
