@@ -128,91 +128,55 @@ __device__ __forceinline__ void group_scale(uint32_t amax_bits, float q, float* 
   }
 }
 
-// 8 values at element i as they lie in memory: 16 or 32 bytes.
-__device__ __forceinline__ void norm_fetch8(const void* p, int64_t i, int dt, bool vec, uint4 (&u)[2]) {
+// f(T()) with T the floating type of the code dt: one branch around all of a
+// row's pieces instead of one in each.
+template <typename F>
+__device__ __forceinline__ void with_type(int dt, F&& f) {
+  if (dt == DT_BF16)
+    f(__nv_bfloat16());
+  else if (dt == DT_FP16)
+    f(__half());
+  else
+    f(0.f);
+}
+
+// 8 values at element i; vec: by 16-byte accesses.
+template <typename T>
+__device__ __forceinline__ void norm_load8(const void* p, int64_t i, bool vec, float (&v)[8]) {
+  const T* q = static_cast<const T*>(p) + i;
   if (vec) {
-    if (dt == DT_FP32) {
-      u[0] = *reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
-      u[1] = *reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i + 4);
-    } else {
-      u[0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-    }
-    return;
-  }
-  if (dt == DT_FP32) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) (&u[e >> 2].x)[e & 3] = static_cast<const uint32_t*>(p)[i + e];
+    load8<T>(q, v);
   } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      (&u[0].x)[e] = static_cast<const uint16_t*>(p)[i + 2 * e] |
-                     (static_cast<uint32_t>(static_cast<const uint16_t*>(p)[i + 2 * e + 1]) << 16);
+    for (int e = 0; e < 8; ++e) v[e] = to_f32<T>(q[e]);
   }
 }
 
-__device__ __forceinline__ void norm_widen8(const uint4 (&u)[2], int dt, float (&v)[8]) {
-  if (dt == DT_FP32) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = __uint_as_float((&u[e >> 2].x)[e & 3]);
-  } else if (dt == DT_BF16) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[2 * e] = __uint_as_float((&u[0].x)[e] << 16);
-      v[2 * e + 1] = __uint_as_float((&u[0].x)[e] & 0xFFFF0000u);
-    }
+template <typename T>
+__device__ __forceinline__ void norm_store8(void* p, int64_t i, bool vec, const float (&v)[8]) {
+  T* q = static_cast<T*>(p) + i;
+  if (vec) {
+    store8<T>(q, v);
   } else {
 #pragma unroll
+    for (int e = 0; e < 8; ++e) q[e] = from_f32<T>(v[e]);
+  }
+}
+
+// Rounds v to T, pairs at a time (the same conversions as store8's).
+template <typename T>
+__device__ __forceinline__ void norm_round8(float (&v)[8]) {
+  if constexpr (!__is_same(T, float)) {
+#pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&(&u[0].x)[e]));
+      float2 f;
+      if constexpr (__is_same(T, __half))
+        f = __half22float2(__floats2half2_rn(v[2 * e], v[2 * e + 1]));
+      else
+        f = __bfloat1622float2(__floats2bfloat162_rn(v[2 * e], v[2 * e + 1]));
       v[2 * e] = f.x;
       v[2 * e + 1] = f.y;
     }
-  }
-}
-
-// v rounded to dt and stored at element i (when `in`); v keeps the rounded values.
-__device__ __forceinline__ void norm_round_store8(void* p, int64_t i, int dt, bool vec, bool in, float (&v)[8]) {
-  uint4 u[2] = {};
-  if (dt == DT_FP32) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) (&u[e >> 2].x)[e & 3] = __float_as_uint(v[e]);
-  } else if (dt == DT_BF16) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
-      (&u[0].x)[e] = *reinterpret_cast<const uint32_t*>(&b);
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const __half2 b = __floats2half2_rn(v[2 * e], v[2 * e + 1]);
-      (&u[0].x)[e] = *reinterpret_cast<const uint32_t*>(&b);
-    }
-  }
-  norm_widen8(u, dt, v);
-  if (!in) return;
-  if (!vec) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) store_from_f32(p, i + e, dt, v[e]);  // exact
-  } else if (dt == DT_FP32) {
-    uint4* q = reinterpret_cast<uint4*>(static_cast<float*>(p) + i);
-    q[0] = u[0];
-    q[1] = u[1];
-  } else {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = u[0];
-  }
-}
-
-__device__ __forceinline__ void norm_store8(void* p, int64_t i, int dt, bool vec, const float (&v)[8]) {
-  if (!vec) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) store_from_f32(p, i + e, dt, v[e]);
-  } else if (dt == DT_FP32) {
-    store8<float>(static_cast<float*>(p) + i, v);
-  } else if (dt == DT_BF16) {
-    store8<__nv_bfloat16>(static_cast<__nv_bfloat16*>(p) + i, v);
-  } else {
-    store8<__half>(static_cast<__half*>(p) + i, v);
   }
 }
 
@@ -295,26 +259,21 @@ __device__ __forceinline__ void norm_fwht(float (&v)[4][8], float* buf, int lane
 // coalesced.
 enum : int { NORM_PIECES = 0, NORM_ROTATED = 1, NORM_STRIDED = 2 };
 
-// The weights from element k on as they lie in memory (ones when there are none),
-// in the rotated kernel with the signs on them.
-template <int kMode>
-__device__ __forceinline__ void norm_weight8(const NormParams& p, int k, uint4 (&u)[2]) {
+// The weights from element k on (ones when there are none), in the rotated kernel
+// with the signs on them: exact in the weights' own type.
+template <typename T, int kMode>
+__device__ __forceinline__ void norm_weight8(const NormParams& p, int k, float (&w)[8]) {
   if (p.weight != nullptr) {
-    norm_fetch8(p.weight, k, p.wt, p.vec, u);
+    norm_load8<T>(p.weight, k, p.vec, w);
   } else {
-    const uint32_t one = p.wt == DT_FP32 ? 0x3F800000u : (p.wt == DT_BF16 ? 0x3F803F80u : 0x3C003C00u);
-    u[0] = u[1] = make_uint4(one, one, one, one);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = 1.f;
   }
   if constexpr (kMode == NORM_ROTATED) {
     const uint2 s = *reinterpret_cast<const uint2*>(p.signs + k);
-    if (p.wt == DT_FP32) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) (&u[e >> 2].x)[e & 3] ^= ((e < 4 ? s.x : s.y) << (24 - 8 * (e & 3))) & 0x80000000u;
-    } else {
-      // signs (e, e + 1) in the top bits of the halves
-#pragma unroll
-      for (int e = 0; e < 4; ++e) (&u[0].x)[e] ^= __byte_perm(e < 2 ? s.x : s.y, 0u, (e & 1) ? 0x3424u : 0x1404u) & 0x80008000u;
-    }
+    for (int e = 0; e < 8; ++e)
+      w[e] = __uint_as_float(__float_as_uint(w[e]) ^ (((e < 4 ? s.x : s.y) << (24 - 8 * (e & 3))) & 0x80000000u));
   }
 }
 
@@ -326,7 +285,7 @@ __device__ __forceinline__ void norm_weight8(const NormParams& p, int k, uint4 (
 constexpr int kNormStages = 1;
 
 template <int NV, int kMode, int kMaxThreads, bool kBulk>
-__global__ void __launch_bounds__(kMaxThreads, 1) rms_norm_kernel(const NormParams p) {
+__global__ void __launch_bounds__(kMaxThreads, kMaxThreads <= 320 ? 2 : 1) rms_norm_kernel(const NormParams p) {
   extern __shared__ __align__(16) float norm_smem[];
   __shared__ uint32_t red[64];
   __shared__ uint64_t bars[kNormStages];
@@ -336,6 +295,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) rms_norm_kernel(const NormPara
   auto at = [&](int j) {
     return kMode == NORM_ROTATED ? 1024 * warp + 256 * j + 8 * lane : (kMode == NORM_PIECES ? 8 * (j * T + tid) : 8 * j * T + tid);
   };
+  auto in = [&](int j) { return kMode == NORM_ROTATED || at(j) < K; };
   uint8_t* weights = reinterpret_cast<uint8_t*>(norm_smem + (kMode == NORM_ROTATED ? (T >> 5) * kNormRotFloats : 0));
   const int w_size = p.wt == DT_FP32 ? 4 : 2;
   uint8_t* stages = weights + K * w_size;
@@ -354,12 +314,12 @@ __global__ void __launch_bounds__(kMaxThreads, 1) rms_norm_kernel(const NormPara
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (at(j) < K) {
-        uint4 w[2];
-        norm_weight8<kMode>(p, at(j), w);
-        uint4* dst = reinterpret_cast<uint4*>(weights + at(j) * w_size);
-        dst[0] = w[0];
-        if (w_size == 4) dst[1] = w[1];
+      if (in(j)) {
+        with_type(p.wt, [&](auto tw) {
+          float w[8];
+          norm_weight8<decltype(tw), kMode>(p, at(j), w);
+          norm_store8<decltype(tw)>(weights, at(j), true, w);
+        });
       }
     __syncthreads();
   }
@@ -405,49 +365,50 @@ __global__ void __launch_bounds__(kMaxThreads, 1) rms_norm_kernel(const NormPara
           }
       }
     } else {
-      if constexpr (kBulk) {
-        // after a wait that gave up the rows are wrong and the fault word says so
-        ok = ok && mbar_wait(&bars[stage], phase, FAULT_WAIT_FULL);
-        const uint8_t* st = stages + stage * (x_bytes + r_bytes);
+      // after a wait that gave up the rows are wrong and the fault word says so
+      if constexpr (kBulk) ok = ok && mbar_wait(&bars[stage], phase, FAULT_WAIT_FULL);
+      const uint8_t* st = stages + stage * (x_bytes + r_bytes);
+      const void* xp = kBulk ? static_cast<const void*>(st) : p.x;
+      const int64_t xbase = kBulk ? 0 : base;
+      const bool vec = kBulk || p.vec;
+      with_type(p.xt, [&](auto tx) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-          uint4 u[2] = {};
-          if (at(j) < K) norm_fetch8(st, at(j), p.xt, true, u);
-          norm_widen8(u, p.xt, v[j]);
-          if (r_bytes != 0) {
-            uint4 w[2] = {};
-            float r[8];
-            if (at(j) < K) norm_fetch8(st + x_bytes, at(j), p.rt, true, w);
-            norm_widen8(w, p.rt, r);
+          if (in(j)) {
+            norm_load8<decltype(tx)>(xp, xbase + at(j), vec, v[j]);
+          } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[j][e] += r[e];
-            norm_round_store8(p.residual_out, base + at(j), p.rt, true, at(j) < K, v[j]);
+            for (int e = 0; e < 8; ++e) v[j][e] = 0.f;
           }
         }
-      } else {
-        // all loads before the first store
-        uint4 xu[NV][2] = {};
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-          if (at(j) < K) norm_fetch8(p.x, base + at(j), p.xt, p.vec, xu[j]);
-        if (p.residual != nullptr) {
-          uint4 ru[NV][2] = {};
-#pragma unroll
-          for (int j = 0; j < NV; ++j)
-            if (at(j) < K) norm_fetch8(p.residual, base + at(j), p.rt, p.vec, ru[j]);
-#pragma unroll
-          for (int j = 0; j < NV; ++j) {
-            float r[8];
-            norm_widen8(xu[j], p.xt, v[j]);
-            norm_widen8(ru[j], p.rt, r);
+      });
+      if (p.residual != nullptr) {
+        const void* rp = kBulk ? static_cast<const void*>(st + x_bytes) : p.residual;
+        with_type(p.rt, [&](auto tr) {
+          auto add = [&](int j, const float (&r)[8]) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[j][e] += r[e];
-            norm_round_store8(p.residual_out, base + at(j), p.rt, p.vec, at(j) < K, v[j]);
-          }
-        } else {
+            norm_round8<decltype(tr)>(v[j]);
+            norm_store8<decltype(tr)>(p.residual_out, base + at(j), vec, v[j]);
+          };
+          if constexpr (kBulk) {
 #pragma unroll
-          for (int j = 0; j < NV; ++j) norm_widen8(xu[j], p.xt, v[j]);
-        }
+            for (int j = 0; j < NV; ++j)
+              if (in(j)) {
+                float r[8];
+                norm_load8<decltype(tr)>(rp, at(j), true, r);
+                add(j, r);
+              }
+          } else {
+            float r[NV][8];  // all loads before the first store
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+              if (in(j)) norm_load8<decltype(tr)>(rp, base + at(j), vec, r[j]);
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+              if (in(j)) add(j, r[j]);
+          }
+        });
       }
     }
     float ss = 0.f;
@@ -487,43 +448,46 @@ __global__ void __launch_bounds__(kMaxThreads, 1) rms_norm_kernel(const NormPara
       inv = static_cast<float>(1.0 / sqrt(ldexp(static_cast<double>(s2) / K, 2 * ex) + static_cast<double>(p.eps)));
     }
     if constexpr (kMode == NORM_ROTATED) inv *= kHNorm;  // the transform's 1/32
+    if constexpr (kMode == NORM_STRIDED) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
+      for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[j][e] *= inv;
-      if constexpr (kMode == NORM_STRIDED) {
-        if (p.weight != nullptr) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int k = at(j) + e * T;
-            if (k < K) v[j][e] *= load_as_f32(p.weight, k, p.wt);
-          }
+        for (int e = 0; e < 8; ++e) {
+          const int k = at(j) + e * T;
+          v[j][e] *= inv;
+          if (p.weight != nullptr && k < K) v[j][e] *= load_as_f32(p.weight, k, p.wt);
         }
-      } else if (at(j) < K) {
-        uint4 u[2] = {};
-        float w[8];
-        if constexpr (kBulk)
-          norm_fetch8(weights, at(j), p.wt, true, u);
-        else
-          norm_weight8<kMode>(p, at(j), u);
-        norm_widen8(u, p.wt, w);
+    } else {
+      with_type(p.wt, [&](auto tw) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[j][e] *= w[e];
-      }
+        for (int j = 0; j < NV; ++j)
+          if (in(j)) {
+            float w[8];
+            if constexpr (kBulk)
+              norm_load8<decltype(tw)>(weights, at(j), true, w);
+            else
+              norm_weight8<decltype(tw), kMode>(p, at(j), w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[j][e] = v[j][e] * inv * w[e];
+          }
+      });
     }
     if constexpr (kMode == NORM_ROTATED) norm_fwht(v, norm_smem + warp * kNormRotFloats, lane);
     if (p.group == 0) {
+      if constexpr (kMode == NORM_STRIDED) {
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        if constexpr (kMode == NORM_STRIDED) {
+        for (int j = 0; j < NV; ++j)
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const int k = at(j) + e * T;
             if (k < K) store_from_f32(p.y, base + k, p.yt, v[j][e]);
           }
-        } else if (at(j) < K) {
-          norm_store8(p.y, base + at(j), p.yt, p.vec, v[j]);
-        }
+      } else {
+        with_type(p.yt, [&](auto ty) {
+#pragma unroll
+          for (int j = 0; j < NV; ++j)
+            if (in(j)) norm_store8<decltype(ty)>(p.y, base + at(j), kBulk || p.vec, v[j]);
+        });
       }
       continue;
     }
@@ -550,7 +514,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) rms_norm_kernel(const NormPara
             const int k = at(j) + e * T;
             if (k < K) y[base + k] = code8(v[j][e] * is, p.yt);
           }
-        } else if (at(j) < K) {
+        } else if (in(j)) {
           norm_store_codes8(y, base + at(j), p.yt, p.vec, v[j], is);
         }
       }
@@ -562,7 +526,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) rms_norm_kernel(const NormPara
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) mb[j] = max(mb[j], __shfl_xor_sync(0xffffffffu, mb[j], o));
         group_scale(mb[j], q, &scale, &is);
-        if (at(j) < K) {
+        if (in(j)) {
           if ((lane & 15) == 0) p.y_scales[row * G + (at(j) >> 7)] = scale;
           norm_store_codes8(y, base + at(j), p.yt, p.vec, v[j], is);
         }

@@ -1163,7 +1163,9 @@ tb_status run_norm(const NormParams& p, const DevInfo* d, cudaStream_t st) {
     const size_t smem = sizeof(float) * kNormRotFloats * warps;
     if (warps > 16) return launch_norm<4, NORM_ROTATED, 1024>(p, d, 32 * warps, smem, st);
     if (norm_bulk(p, d, smem + norm_stage_bytes(p)))
-      return launch_norm<4, NORM_ROTATED, 512, true>(p, d, 32 * warps, smem + norm_stage_bytes(p), st);
+      // up to 320 threads: 96 registers, so that four blocks of a 5120-wide row fit an SM
+      return warps <= 10 ? launch_norm<4, NORM_ROTATED, 320, true>(p, d, 32 * warps, smem + norm_stage_bytes(p), st)
+                         : launch_norm<4, NORM_ROTATED, 512, true>(p, d, 32 * warps, smem + norm_stage_bytes(p), st);
     return launch_norm<4, NORM_ROTATED, 512>(p, d, 32 * warps, smem, st);
   }
   return p.K % 8 == 0 ? run_norm_pieces<NORM_PIECES>(p, d, st) : run_norm_pieces<NORM_STRIDED>(p, d, st);
