@@ -25,6 +25,7 @@
 #include "pack.cuh"
 #include "q4.cuh"
 #include "q4_linear.cuh"
+#include "q4_mid.cuh"
 #include "simple.cuh"
 
 namespace {
@@ -163,6 +164,30 @@ tb_status launch_pdl(Kern kern, dim3 grid, dim3 block, size_t smem, cudaStream_t
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) {
+    cudaGetLastError();
+    return TB_ERR_CUDA;
+  }
+  return TB_OK;
+}
+
+// launch_pdl with clusters of S blocks.
+template <typename Kern, typename... Args>
+tb_status launch_cluster(Kern kern, dim3 grid, dim3 block, size_t smem, int S, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(S);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = S > 1 ? 2 : 1;
   if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) {
     cudaGetLastError();
     return TB_ERR_CUDA;
@@ -1287,6 +1312,37 @@ tb_status run_q4_gemm(const Q4Args& a, const DevInfo* d) {
   }
 }
 
+// The cluster size of the 17-128-token kernel: K of a 128-row tile is split while
+// the tiles leave SMs free, into at most 8 and at most a CTA per two 128-groups.
+// Clusters do not cross GPCs, so not every SM can be had: 16 of 18 is assumed.
+int q4_mid_split(int64_t N, int64_t K, int sm_count) {
+  const int64_t tiles = (N + 127) / 128, G = K / 128;
+  int S = 1;
+  while (S < 8 && tiles * (S + 1) <= sm_count * 16 / 18 && G >= 2 * (S + 1)) ++S;
+  return S;
+}
+
+template <int BT>
+tb_status run_q4_mid(const Q4Args& a, const DevInfo* d) {
+  __half* xh = static_cast<__half*>(a.ws);
+  float* factor = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + q4_x_bytes(a.M, a.K));
+  CUtensorMap tm_x, tm_w;
+  if (make_map_2d(&tm_x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, xh, a.K, a.M, a.K * 2, 64, BT, CU_TENSOR_MAP_SWIZZLE_128B) !=
+          TB_OK ||
+      make_map_2d(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.packed, a.K / 2, a.N, a.K / 2, 128, 128,
+                  CU_TENSOR_MAP_SWIZZLE_128B) != TB_OK)
+    return TB_ERR_CUDA;
+  auto k = q4_mid_kernel<BT>;
+  if (allow_smem(k, d) != TB_OK) return TB_ERR_CUDA;
+  const tb_status st = run_q4_prep(a, xh, factor);
+  if (st != TB_OK) return st;
+  const int S = q4_mid_split(a.N, a.K, d->sm_count);
+  const Q4MidParams p{static_cast<int>(a.M), static_cast<int>(a.N), static_cast<int>(a.K), S, a.yt, a.y, a.scales, factor};
+  const int64_t tiles = (a.N + 127) / 128;
+  return launch_cluster(k, dim3(static_cast<unsigned>(tiles * S)), dim3(kQmThreads), static_cast<size_t>(qm_smem_bytes(BT)),
+                        S, a.st, tm_x, tm_w, p);
+}
+
 struct Q4DecodePlan {
   int NT, C, P, rw, nblocks, Wt, Wk, S, Gs, clusters, part_at;
   size_t smem;
@@ -1335,25 +1391,8 @@ tb_status launch_q4_decode(const CUtensorMap& tm, const Q4DecodeParams& p, const
                            cudaStream_t st) {
   auto k = q4_decode_kernel<NT>;
   if (allow_smem(k, d) != TB_OK) return TB_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(pl.S * std::min(pl.clusters, pl.nblocks)));
-  cfg.blockDim = dim3(32 * kQ4DecWarps);
-  cfg.dynamicSmemBytes = pl.smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(pl.S);
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = pl.S > 1 ? 2 : 1;
-  if (cudaLaunchKernelEx(&cfg, k, tm, p) != cudaSuccess) {
-    cudaGetLastError();
-    return TB_ERR_CUDA;
-  }
-  return TB_OK;
+  return launch_cluster(k, dim3(static_cast<unsigned>(pl.S * std::min(pl.clusters, pl.nblocks))), dim3(32 * kQ4DecWarps),
+                        pl.smem, pl.S, st, tm, p);
 }
 
 tb_status run_q4_decode(const Q4Args& a, const DevInfo* d, const Q4DecodePlan& pl) {
@@ -1408,6 +1447,9 @@ tb_status run_q4(const Q4Args& a, const DevInfo* d) {
     if (q4_decode_plan(a.N, a.K, static_cast<int>(a.M), P, copied, d->sm_count, d->max_smem_optin, &pl))
       return run_q4_decode(a, d, pl);
   }
+  if (a.M <= 32) return run_q4_mid<32>(a, d);
+  if (a.M <= 64) return run_q4_mid<64>(a, d);
+  if (a.M <= 128) return run_q4_mid<128>(a, d);
   return run_q4_gemm(a, d);
 }
 
