@@ -18,7 +18,8 @@ namespace tb {
 // a block's sums can grow 32-fold), so that bf16 rows of any size keep their 8
 // bits in fp16; an 8-bit row with one scale is exact as it is and its scale is
 // the factor.  Values below 2^-29 of the row's largest lose bits.
-// One block of 128 threads a row; two passes over it (the second hits L2).
+// One block a row, a thread for 8 values up to 8192 of them; longer rows are read
+// twice (the second time from L2).
 template <typename TIn>
 __device__ __forceinline__ void q4_load8(const TIn* p, float v[8]) { load8<TIn>(p, v); }
 template <>
@@ -38,29 +39,37 @@ __device__ __forceinline__ void q4_load8<__nv_fp8_e4m3>(const __nv_fp8_e4m3* p, 
 }
 
 template <typename TIn>
-__global__ void __launch_bounds__(kHThreads)
+__global__ void __launch_bounds__(1024)
     q4_prep_kernel(const TIn* __restrict__ x, const float* __restrict__ x_scales, int group,
                    const int8_t* __restrict__ signs, __half* __restrict__ out, float* __restrict__ factor, int K) {
   constexpr bool k8 = sizeof(TIn) == 1;
-  __shared__ float sm[kHB];
+  extern __shared__ __align__(16) float prep_smem[];  // rotated: 1024 floats per 128 threads
   __shared__ uint32_t red[64];
   pdl_launch_dependents();
   const int64_t row = blockIdx.x;
-  const int tid = threadIdx.x, G = K / 128;
+  const int tid = threadIdx.x, T = blockDim.x, G = K / 128;
   const TIn* xr = x + row * K;
-  // the largest magnitude of the row as fp32 bits (NaN and infinity above all)
-  float f = 1.f;    // x' = x f
+  float f = 1.f;      // x' = x f
   float out_f = 1.f;  // x = x' out_f
+  float v[8];
+  pdl_wait();
+  if (8 * tid < K) q4_load8<TIn>(xr + 8 * tid, v);
   if (!k8 || group == 128) {
+    // the largest magnitude of the row as fp32 bits (NaN and infinity above all)
     uint32_t mb = 0;
     if constexpr (k8) {
-      for (int g = tid; g < G; g += kHThreads) mb = max(mb, abs_bits(x_scales[row * G + g] * 448.f));
+      for (int g = tid; g < G; g += T) mb = max(mb, abs_bits(x_scales[row * G + g] * 448.f));
     } else {
-      for (int k = 8 * tid; k < K; k += 8 * kHThreads) {
-        float v[8];
-        q4_load8<TIn>(xr + k, v);
+      for (int k = 8 * tid; k < K; k += 8 * T) {
+        float u[8];
+        if (k == 8 * tid) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) mb = max(mb, abs_bits(v[i]));
+          for (int i = 0; i < 8; ++i) u[i] = v[i];
+        } else {
+          q4_load8<TIn>(xr + k, u);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mb = max(mb, abs_bits(u[i]));
       }
     }
     mb = BlockReduce{red, 0}.max_bits(mb);
@@ -73,9 +82,8 @@ __global__ void __launch_bounds__(kHThreads)
     out_f = x_scales[row];
   }
   if (tid == 0) factor[row] = out_f;
-  for (int k = 8 * tid; k < K; k += 8 * kHThreads) {
-    float v[8];
-    q4_load8<TIn>(xr + k, v);
+  for (int k = 8 * tid; k < K; k += 8 * T) {
+    if (k != 8 * tid) q4_load8<TIn>(xr + k, v);
     float c = f;
     if constexpr (k8) {
       if (group == 128) c *= x_scales[row * G + (k >> 7)];
@@ -83,12 +91,12 @@ __global__ void __launch_bounds__(kHThreads)
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] *= c;
     if constexpr (!k8) {
-      if (signs != nullptr) {
+      if (signs != nullptr) {  // T is a multiple of 128 and K of 1024: whole groups of 128 threads
         float d[8];
         load_signs8(signs + k, d);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] *= d[i];
-        fwht1024(v, sm);
+        fwht1024_group(v, prep_smem + 1024 * (tid >> 7), tid & 127, 1 + (tid >> 7));
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] *= kHNorm;
       }
@@ -241,6 +249,7 @@ __global__ void __launch_bounds__(kHThreads)
                      int K, int P, int C) {
   __shared__ __align__(16) float sm[kHB + 8 * 32];  // 32 values and 8 of padding a lane
   pdl_launch_dependents();
+  pdl_wait();
   const int tid = threadIdx.x, m = blockIdx.y, G = K / 128;
   const int k = blockIdx.x * kHB + 8 * tid;
   float v[8] = {};

@@ -1247,20 +1247,21 @@ tb_status validate_q4(const Q4Args& a) {
 }
 
 template <typename TIn>
-void launch_q4_prep(const Q4Args& a, __half* xh, float* factor) {
-  q4_prep_kernel<TIn><<<static_cast<unsigned>(a.M), kHThreads, 0, a.st>>>(
-      static_cast<const TIn*>(a.x), a.x_scales, static_cast<int>(a.x_group), a.signs, xh, factor,
-      static_cast<int>(a.K));
+tb_status launch_q4_prep(const Q4Args& a, __half* xh, float* factor) {
+  const int unit = a.signs != nullptr ? 128 : 32;  // rotated: 128 threads a 1024-block
+  const int threads = static_cast<int>(std::min<int64_t>(1024, (a.K / 8 + unit - 1) / unit * unit));
+  return launch_pdl(q4_prep_kernel<TIn>, dim3(static_cast<unsigned>(a.M)), dim3(static_cast<unsigned>(threads)),
+                    a.signs != nullptr ? sizeof(float) * 8 * threads : size_t(0), a.st, static_cast<const TIn*>(a.x),
+                    a.x_scales, static_cast<int>(a.x_group), a.signs, xh, factor, static_cast<int>(a.K));
 }
 
 tb_status run_q4_prep(const Q4Args& a, __half* xh, float* factor) {
   switch (a.xt) {
-    case TB_BF16: launch_q4_prep<__nv_bfloat16>(a, xh, factor); break;
-    case TB_FP16: launch_q4_prep<__half>(a, xh, factor); break;
-    case TB_INT8: launch_q4_prep<int8_t>(a, xh, factor); break;
-    default: launch_q4_prep<__nv_fp8_e4m3>(a, xh, factor); break;
+    case TB_BF16: return launch_q4_prep<__nv_bfloat16>(a, xh, factor);
+    case TB_FP16: return launch_q4_prep<__half>(a, xh, factor);
+    case TB_INT8: return launch_q4_prep<int8_t>(a, xh, factor);
+    default: return launch_q4_prep<__nv_fp8_e4m3>(a, xh, factor);
   }
-  return launch_status();
 }
 
 template <int BT, typename TOut>
@@ -1424,9 +1425,10 @@ tb_status run_q4_decode(const Q4Args& a, const DevInfo* d, const Q4DecodePlan& p
     uint4* image = static_cast<uint4*>(a.ws);
     const int64_t G = a.K / 128;
     float* factors = reinterpret_cast<float*>(image + G * 8 * pl.C);
-    q4_planes_kernel<<<dim3(static_cast<unsigned>((a.K + kHB - 1) / kHB), static_cast<unsigned>(a.M)), kHThreads, 0,
-                       a.st>>>(a.x, p.xmode, a.x_scales, p.x_group, a.signs, image, factors, p.M, p.K, pl.P, pl.C);
-    if (launch_status() != TB_OK) return TB_ERR_CUDA;
+    if (launch_pdl(q4_planes_kernel, dim3(static_cast<unsigned>((a.K + kHB - 1) / kHB), static_cast<unsigned>(a.M)),
+                   dim3(kHThreads), 0, a.st, a.x, p.xmode, a.x_scales, p.x_group, a.signs, image, factors, p.M, p.K, pl.P,
+                   pl.C) != TB_OK)
+      return TB_ERR_CUDA;
     p.x = image;
     p.x_scales = factors;
     p.xmode = Q4X_IMAGE;
@@ -1770,17 +1772,19 @@ tb_status tb_q4_prepare_weights(const void* w, tb_dtype wt, const int8_t* signs,
   const cudaStream_t s = as_stream(stream);
   const unsigned grid = static_cast<unsigned>(blocks);
   const int block = 32 * kPwWarps, k = static_cast<int>(K);
+#define TB_Q4P(T)                                                                                             \
+  do {                                                                                                        \
+    if (signs != nullptr)                                                                                     \
+      q4_fold_kernel<<<grid, block, 0, s>>>(static_cast<const T*>(w), signs, packed, scales, N, k);           \
+    else                                                                                                      \
+      q4_round_kernel<<<grid, block, 0, s>>>(static_cast<const T*>(w), packed, scales, N, k, aligned(w, 16)); \
+  } while (0)
   switch (wt) {
-    case TB_BF16:
-      q4_prepare_kernel<<<grid, block, 0, s>>>(static_cast<const __nv_bfloat16*>(w), signs, packed, scales, N, k);
-      break;
-    case TB_FP16:
-      q4_prepare_kernel<<<grid, block, 0, s>>>(static_cast<const __half*>(w), signs, packed, scales, N, k);
-      break;
-    default:
-      q4_prepare_kernel<<<grid, block, 0, s>>>(static_cast<const float*>(w), signs, packed, scales, N, k);
-      break;
+    case TB_BF16: TB_Q4P(__nv_bfloat16); break;
+    case TB_FP16: TB_Q4P(__half); break;
+    default: TB_Q4P(float); break;
   }
+#undef TB_Q4P
   return launch_status();
 }
 
