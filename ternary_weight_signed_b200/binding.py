@@ -94,10 +94,17 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_raw_stream = None  # (device index) -> handle of its current stream, without a Stream object
+
+
 def _stream(stream):
     if stream is None:
+        global _raw_stream
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None:
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+                lambda d: torch.cuda.current_stream(d).cuda_stream)
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
