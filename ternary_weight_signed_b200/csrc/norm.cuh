@@ -296,6 +296,13 @@ __global__ void __launch_bounds__(kMaxThreads, kMaxThreads <= 320 ? 2 : 1) rms_n
     return kMode == NORM_ROTATED ? 1024 * warp + 256 * j + 8 * lane : (kMode == NORM_PIECES ? 8 * (j * T + tid) : 8 * j * T + tid);
   };
   auto in = [&](int j) { return kMode == NORM_ROTATED || at(j) < K; };
+  // f(piece, value, element) over the thread's values, strided layout
+  auto each = [&](auto&& f) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f(j, e, at(j) + e * T);
+  };
   uint8_t* weights = reinterpret_cast<uint8_t*>(norm_smem + (kMode == NORM_ROTATED ? (T >> 5) * kNormRotFloats : 0));
   const int w_size = p.wt == DT_FP32 ? 4 : 2;
   uint8_t* stages = weights + K * w_size;
@@ -339,30 +346,22 @@ __global__ void __launch_bounds__(kMaxThreads, kMaxThreads <= 320 ? 2 : 1) rms_n
     const int64_t base = row * K;
     float v[NV][8];
     if constexpr (kMode == NORM_STRIDED) {
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int k = at(j) + e * T;
-          v[j][e] = k < K ? load_as_f32(p.x, base + k, p.xt) : 0.f;
-        }
+      with_type(p.xt, [&](auto tx) {
+        const decltype(tx)* src = static_cast<const decltype(tx)*>(p.x) + base;
+        each([&](int j, int e, int k) { v[j][e] = k < K ? to_f32(src[k]) : 0.f; });
+      });
       if (p.residual != nullptr) {
-        float r[NV][8];
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int k = at(j) + e * T;
-            r[j][e] = k < K ? load_as_f32(p.residual, base + k, p.rt) : 0.f;
-          }
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int k = at(j) + e * T;
-            v[j][e] = round_to(v[j][e] + r[j][e], p.rt);
-            if (k < K) store_from_f32(p.residual_out, base + k, p.rt, v[j][e]);
-          }
+        with_type(p.rt, [&](auto tr) {
+          using TR = decltype(tr);
+          const TR* src = static_cast<const TR*>(p.residual) + base;
+          TR* dst = static_cast<TR*>(p.residual_out) + base;
+          each([&](int j, int e, int k) { v[j][e] += k < K ? to_f32(src[k]) : 0.f; });  // all loads before the first store
+          each([&](int j, int e, int k) {
+            const TR h = from_f32<TR>(v[j][e]);
+            v[j][e] = to_f32(h);
+            if (k < K) dst[k] = h;
+          });
+        });
       }
     } else {
       // after a wait that gave up the rows are wrong and the fault word says so
@@ -449,14 +448,14 @@ __global__ void __launch_bounds__(kMaxThreads, kMaxThreads <= 320 ? 2 : 1) rms_n
     }
     if constexpr (kMode == NORM_ROTATED) inv *= kHNorm;  // the transform's 1/32
     if constexpr (kMode == NORM_STRIDED) {
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int k = at(j) + e * T;
-          v[j][e] *= inv;
-          if (p.weight != nullptr && k < K) v[j][e] *= load_as_f32(p.weight, k, p.wt);
-        }
+      each([&](int j, int e, int) { v[j][e] *= inv; });
+      if (p.weight != nullptr)
+        with_type(p.wt, [&](auto tw) {
+          const decltype(tw)* src = static_cast<const decltype(tw)*>(p.weight);
+          each([&](int j, int e, int k) {
+            if (k < K) v[j][e] *= to_f32(src[k]);
+          });
+        });
     } else {
       with_type(p.wt, [&](auto tw) {
 #pragma unroll
@@ -475,13 +474,12 @@ __global__ void __launch_bounds__(kMaxThreads, kMaxThreads <= 320 ? 2 : 1) rms_n
     if constexpr (kMode == NORM_ROTATED) norm_fwht(v, norm_smem + warp * kNormRotFloats, lane);
     if (p.group == 0) {
       if constexpr (kMode == NORM_STRIDED) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int k = at(j) + e * T;
-            if (k < K) store_from_f32(p.y, base + k, p.yt, v[j][e]);
-          }
+        with_type(p.yt, [&](auto ty) {
+          decltype(ty)* dst = static_cast<decltype(ty)*>(p.y) + base;
+          each([&](int j, int e, int k) {
+            if (k < K) dst[k] = from_f32<decltype(ty)>(v[j][e]);
+          });
+        });
       } else {
         with_type(p.yt, [&](auto ty) {
 #pragma unroll
@@ -506,17 +504,19 @@ __global__ void __launch_bounds__(kMaxThreads, kMaxThreads <= 320 ? 2 : 1) rms_n
       for (int j = 1; j < NV; ++j) mb[0] = max(mb[0], mb[j]);
       group_scale(reduce.max_bits(mb[0]), q, &scale, &is);
       if (tid == 0) p.y_scales[row] = scale;
+      if constexpr (kMode == NORM_STRIDED) {
+        if (p.yt == DT_INT8)
+          each([&](int j, int e, int k) {
+            if (k < K) y[base + k] = code8(v[j][e] * is, DT_INT8);
+          });
+        else
+          each([&](int j, int e, int k) {
+            if (k < K) y[base + k] = code8(v[j][e] * is, DT_E4M3);
+          });
+      } else {
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        if constexpr (kMode == NORM_STRIDED) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int k = at(j) + e * T;
-            if (k < K) y[base + k] = code8(v[j][e] * is, p.yt);
-          }
-        } else if (in(j)) {
-          norm_store_codes8(y, base + at(j), p.yt, p.vec, v[j], is);
-        }
+        for (int j = 0; j < NV; ++j)
+          if (in(j)) norm_store_codes8(y, base + at(j), p.yt, p.vec, v[j], is);
       }
     } else if constexpr (kMode != NORM_STRIDED) {
       // groups of 128: 16 lanes of a piece

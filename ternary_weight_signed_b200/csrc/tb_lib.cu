@@ -1157,14 +1157,16 @@ size_t norm_stage_bytes(const NormParams& p) {
 
 template <int kMode>
 tb_status run_norm_pieces(const NormParams& p, const DevInfo* d, cudaStream_t st) {
-  // pieces of a thread: one where a row is alone on its SM (latency), else up to
-  // four (more bytes in flight a thread, fewer barriers a byte)
+  // pieces of a thread: one where a row is alone on its SM (latency), else two, or
+  // up to four when the rows come by bulk copies (more bytes in flight a thread,
+  // fewer barriers a byte; without the copies four would spill)
   const int pieces = (p.K + 7) / 8;
+  const bool many = p.M > 2 * d->sm_count;
   int nv = 1;
-  while (nv < 4 && (pieces > 1024 * nv || (p.M > 2 * d->sm_count && pieces >= 256 * nv))) nv *= 2;
-  const int threads = ((pieces + nv - 1) / nv + 31) / 32 * 32;
+  while (nv < 4 && (pieces > 1024 * nv || (many && pieces >= 256 * nv))) nv *= 2;
   if constexpr (kMode == NORM_PIECES) {
     const size_t smem = norm_stage_bytes(p);
+    const int threads = ((pieces + nv - 1) / nv + 31) / 32 * 32;
     if (threads <= 512 && norm_bulk(p, d, smem)) {
       switch (nv) {
         case 1: return launch_norm<1, kMode, 512, true>(p, d, threads, smem, st);
@@ -1173,12 +1175,12 @@ tb_status run_norm_pieces(const NormParams& p, const DevInfo* d, cudaStream_t st
       }
     }
   }
+  if (nv == 4 && pieces <= 2048) nv = 2;
+  const int threads = ((pieces + nv - 1) / nv + 31) / 32 * 32;
   switch (nv) {
     case 1: return launch_norm<1, kMode, 1024>(p, d, threads, 0, st);
     case 2: return launch_norm<2, kMode, 1024>(p, d, threads, 0, st);
-    default:
-      return threads <= 512 ? launch_norm<4, kMode, 512>(p, d, threads, 0, st)
-                            : launch_norm<4, kMode, 1024>(p, d, threads, 0, st);
+    default: return launch_norm<4, kMode, 1024>(p, d, threads, 0, st);
   }
 }
 
