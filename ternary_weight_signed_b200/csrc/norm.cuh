@@ -20,33 +20,16 @@
 
 namespace tb {
 
-constexpr int kNormMaxK = 32768;
 constexpr int kNormRotFloats = 4 * 264;  // a warp's transpose buffer: 8 floats of padding every 256
 
 // dtype codes of the C ABI as the kernels get them
 enum : int { DT_BF16 = 0, DT_FP16 = 1, DT_FP32 = 2, DT_INT8 = 3, DT_E4M3 = 5 };
-
-__device__ __forceinline__ float load_as_f32(const void* p, int64_t i, int dt) {
-  switch (dt) {
-    case DT_BF16: return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-    case DT_FP16: return __half2float(static_cast<const __half*>(p)[i]);
-    default: return static_cast<const float*>(p)[i];
-  }
-}
 
 __device__ __forceinline__ void store_from_f32(void* p, int64_t i, int dt, float v) {
   switch (dt) {
     case DT_BF16: static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v); break;
     case DT_FP16: static_cast<__half*>(p)[i] = __float2half_rn(v); break;
     default: static_cast<float*>(p)[i] = v; break;
-  }
-}
-
-__device__ __forceinline__ float round_to(float v, int dt) {
-  switch (dt) {
-    case DT_BF16: return __bfloat162float(__float2bfloat16_rn(v));
-    case DT_FP16: return __half2float(__float2half_rn(v));
-    default: return v;
   }
 }
 
@@ -72,7 +55,7 @@ struct NormParams {
   int group;  // 0: floating output
   int xt, rt, wt, yt;
   float eps;
-  bool vec;  // every pointer allows 16-byte accesses (K % 8 == 0)
+  bool vec;  // every pointer that is read or written in pieces starts on 16 bytes
 };
 
 // Largest absolute value as its fp32 bits: NaN above infinity above the rest.
@@ -160,6 +143,29 @@ __device__ __forceinline__ void norm_store8(void* p, int64_t i, bool vec, const 
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) q[e] = from_f32<T>(v[e]);
+  }
+}
+
+// The values k0 .. k0 + 7 of a row of K at element base, those outside it zero.
+template <typename T>
+__device__ __forceinline__ void norm_load_cut(const void* p, int64_t base, int k0, int K, bool vec, float (&v)[8]) {
+  if (k0 >= 0 && k0 + 8 <= K) {
+    norm_load8<T>(p, base + k0, vec, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      v[e] = k0 + e >= 0 && k0 + e < K ? to_f32<T>(static_cast<const T*>(p)[base + k0 + e]) : 0.f;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void norm_store_cut(void* p, int64_t base, int k0, int K, bool vec, const float (&v)[8]) {
+  if (k0 >= 0 && k0 + 8 <= K) {
+    norm_store8<T>(p, base + k0, vec, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (k0 + e >= 0 && k0 + e < K) static_cast<T*>(p)[base + k0 + e] = from_f32<T>(v[e]);
   }
 }
 
@@ -254,10 +260,11 @@ __device__ __forceinline__ void norm_fwht(float (&v)[4][8], float* buf, int lane
 }
 
 // Layouts of a row over the threads: a piece is 8 consecutive values, piece j of
-// thread t at 8 (j T + t) (rotated: at 1024 warp + 256 j + 8 lane); strided
-// (K % 8 != 0): the values (8 j + e) T + t, so that a warp's scalar accesses stay
-// coalesced.
-enum : int { NORM_PIECES = 0, NORM_ROTATED = 1, NORM_STRIDED = 2 };
+// thread t at 8 (j T + t) (rotated: at 1024 warp + 256 j + 8 lane).  Shifted (K % 8
+// != 0): pieces are cut at multiples of 8 of the element's number in the whole
+// tensor, so that those inside a row are 16-byte accesses whatever its start, and only
+// a row's first and last piece go value by value.
+enum : int { NORM_PIECES = 0, NORM_ROTATED = 1, NORM_SHIFTED = 2 };
 
 // The weights from element k on (ones when there are none), in the rotated kernel
 // with the signs on them: exact in the weights' own type.
@@ -292,17 +299,11 @@ __global__ void __launch_bounds__(kMaxThreads, kMaxThreads <= 320 ? 2 : 1) rms_n
   pdl_launch_dependents();
   const int tid = threadIdx.x, T = blockDim.x, warp = tid >> 5, lane = tid & 31, K = p.K;
   BlockReduce reduce{red, 0};
+  int cut = 0;  // shifted: values of the row's first piece that belong to the row before
   auto at = [&](int j) {
-    return kMode == NORM_ROTATED ? 1024 * warp + 256 * j + 8 * lane : (kMode == NORM_PIECES ? 8 * (j * T + tid) : 8 * j * T + tid);
+    return kMode == NORM_ROTATED ? 1024 * warp + 256 * j + 8 * lane : 8 * (j * T + tid) - cut;
   };
   auto in = [&](int j) { return kMode == NORM_ROTATED || at(j) < K; };
-  // f(piece, value, element) over the thread's values, strided layout
-  auto each = [&](auto&& f) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f(j, e, at(j) + e * T);
-  };
   uint8_t* weights = reinterpret_cast<uint8_t*>(norm_smem + (kMode == NORM_ROTATED ? (T >> 5) * kNormRotFloats : 0));
   const int w_size = p.wt == DT_FP32 ? 4 : 2;
   uint8_t* stages = weights + K * w_size;
@@ -345,22 +346,24 @@ __global__ void __launch_bounds__(kMaxThreads, kMaxThreads <= 320 ? 2 : 1) rms_n
   for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x) {
     const int64_t base = row * K;
     float v[NV][8];
-    if constexpr (kMode == NORM_STRIDED) {
+    if constexpr (kMode == NORM_SHIFTED) {
+      cut = static_cast<int>(base & 7);
       with_type(p.xt, [&](auto tx) {
-        const decltype(tx)* src = static_cast<const decltype(tx)*>(p.x) + base;
-        each([&](int j, int e, int k) { v[j][e] = k < K ? to_f32(src[k]) : 0.f; });
+#pragma unroll
+        for (int j = 0; j < NV; ++j) norm_load_cut<decltype(tx)>(p.x, base, at(j), K, p.vec, v[j]);
       });
       if (p.residual != nullptr) {
         with_type(p.rt, [&](auto tr) {
-          using TR = decltype(tr);
-          const TR* src = static_cast<const TR*>(p.residual) + base;
-          TR* dst = static_cast<TR*>(p.residual_out) + base;
-          each([&](int j, int e, int k) { v[j][e] += k < K ? to_f32(src[k]) : 0.f; });  // all loads before the first store
-          each([&](int j, int e, int k) {
-            const TR h = from_f32<TR>(v[j][e]);
-            v[j][e] = to_f32(h);
-            if (k < K) dst[k] = h;
-          });
+          float r[NV][8];  // all loads before the first store
+#pragma unroll
+          for (int j = 0; j < NV; ++j) norm_load_cut<decltype(tr)>(p.residual, base, at(j), K, p.vec, r[j]);
+#pragma unroll
+          for (int j = 0; j < NV; ++j) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[j][e] += r[j][e];
+            norm_round8<decltype(tr)>(v[j]);
+            norm_store_cut<decltype(tr)>(p.residual_out, base, at(j), K, p.vec, v[j]);
+          }
         });
       }
     } else {
@@ -447,14 +450,21 @@ __global__ void __launch_bounds__(kMaxThreads, kMaxThreads <= 320 ? 2 : 1) rms_n
       inv = static_cast<float>(1.0 / sqrt(ldexp(static_cast<double>(s2) / K, 2 * ex) + static_cast<double>(p.eps)));
     }
     if constexpr (kMode == NORM_ROTATED) inv *= kHNorm;  // the transform's 1/32
-    if constexpr (kMode == NORM_STRIDED) {
-      each([&](int j, int e, int) { v[j][e] *= inv; });
+    if constexpr (kMode == NORM_SHIFTED) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[j][e] *= inv;
       if (p.weight != nullptr)
         with_type(p.wt, [&](auto tw) {
           const decltype(tw)* src = static_cast<const decltype(tw)*>(p.weight);
-          each([&](int j, int e, int k) {
-            if (k < K) v[j][e] *= to_f32(src[k]);
-          });
+#pragma unroll
+          for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int k = at(j) + e;
+              if (k >= 0 && k < K) v[j][e] *= to_f32(src[k]);
+            }
         });
     } else {
       with_type(p.wt, [&](auto tw) {
@@ -473,12 +483,10 @@ __global__ void __launch_bounds__(kMaxThreads, kMaxThreads <= 320 ? 2 : 1) rms_n
     }
     if constexpr (kMode == NORM_ROTATED) norm_fwht(v, norm_smem + warp * kNormRotFloats, lane);
     if (p.group == 0) {
-      if constexpr (kMode == NORM_STRIDED) {
+      if constexpr (kMode == NORM_SHIFTED) {
         with_type(p.yt, [&](auto ty) {
-          decltype(ty)* dst = static_cast<decltype(ty)*>(p.y) + base;
-          each([&](int j, int e, int k) {
-            if (k < K) dst[k] = from_f32<decltype(ty)>(v[j][e]);
-          });
+#pragma unroll
+          for (int j = 0; j < NV; ++j) norm_store_cut<decltype(ty)>(p.y, base, at(j), K, p.vec, v[j]);
         });
       } else {
         with_type(p.yt, [&](auto ty) {
@@ -504,21 +512,23 @@ __global__ void __launch_bounds__(kMaxThreads, kMaxThreads <= 320 ? 2 : 1) rms_n
       for (int j = 1; j < NV; ++j) mb[0] = max(mb[0], mb[j]);
       group_scale(reduce.max_bits(mb[0]), q, &scale, &is);
       if (tid == 0) p.y_scales[row] = scale;
-      if constexpr (kMode == NORM_STRIDED) {
-        if (p.yt == DT_INT8)
-          each([&](int j, int e, int k) {
-            if (k < K) y[base + k] = code8(v[j][e] * is, DT_INT8);
-          });
-        else
-          each([&](int j, int e, int k) {
-            if (k < K) y[base + k] = code8(v[j][e] * is, DT_E4M3);
-          });
+      if constexpr (kMode == NORM_SHIFTED) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          if (at(j) >= 0 && at(j) + 8 <= K) {
+            norm_store_codes8(y, base + at(j), p.yt, p.vec, v[j], is);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (at(j) + e >= 0 && at(j) + e < K) y[base + at(j) + e] = code8(v[j][e] * is, p.yt);
+          }
+        }
       } else {
 #pragma unroll
         for (int j = 0; j < NV; ++j)
           if (in(j)) norm_store_codes8(y, base + at(j), p.yt, p.vec, v[j], is);
       }
-    } else if constexpr (kMode != NORM_STRIDED) {
+    } else if constexpr (kMode != NORM_SHIFTED) {
       // groups of 128: 16 lanes of a piece
       const int64_t G = K / 128;
 #pragma unroll

@@ -1160,7 +1160,7 @@ tb_status run_norm_pieces(const NormParams& p, const DevInfo* d, cudaStream_t st
   // pieces of a thread: one where a row is alone on its SM (latency), else two, or
   // up to four when the rows come by bulk copies (more bytes in flight a thread,
   // fewer barriers a byte; without the copies four would spill)
-  const int pieces = (p.K + 7) / 8;
+  const int pieces = (p.K + 7) / 8 + (kMode == NORM_SHIFTED ? 1 : 0);
   const bool many = p.M > 2 * d->sm_count;
   int nv = 1;
   while (nv < 4 && (pieces > 1024 * nv || (many && pieces >= 256 * nv))) nv *= 2;
@@ -1195,7 +1195,7 @@ tb_status run_norm(const NormParams& p, const DevInfo* d, cudaStream_t st) {
                          : launch_norm<4, NORM_ROTATED, 512, true>(p, d, 32 * warps, smem + norm_stage_bytes(p), st);
     return launch_norm<4, NORM_ROTATED, 512>(p, d, 32 * warps, smem, st);
   }
-  return p.K % 8 == 0 ? run_norm_pieces<NORM_PIECES>(p, d, st) : run_norm_pieces<NORM_STRIDED>(p, d, st);
+  return p.K % 8 == 0 ? run_norm_pieces<NORM_PIECES>(p, d, st) : run_norm_pieces<NORM_SHIFTED>(p, d, st);
 }
 
 // ------------------------------------------------------------------ 4-bit linear
@@ -1718,9 +1718,10 @@ tb_status tb_rms_norm(const void* x, tb_dtype xt, const void* residual, void* re
   const DevInfo* d = nullptr;
   const tb_status st = current_device(&d);
   if (st != TB_OK) return st;
-  const bool vec = K % 8 == 0 && aligned(x, 16) && aligned(y, y8 ? 8 : 16) &&
+  // (weights are read value by value where K % 8 != 0)
+  const bool vec = aligned(x, 16) && aligned(y, y8 ? 8 : 16) &&
                    (residual == nullptr || (aligned(residual, 16) && aligned(residual_out, 16))) &&
-                   (weight == nullptr || aligned(weight, 16));
+                   (weight == nullptr || K % 8 != 0 || aligned(weight, 16));
   const NormParams p{x, residual, residual_out, weight, signs, y, y_scales, M, static_cast<int>(K),
                      static_cast<int>(scale_group), xt, rt, weight == nullptr ? TB_BF16 : wt, yt, eps, vec};
   return run_norm(p, d, as_stream(stream));

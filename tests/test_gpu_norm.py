@@ -147,9 +147,13 @@ def test_eight_bits(yt, m, k, grouped, signs, xt, rt):
     (2600, 1024, "fp32", None, False, "fp16", False), (1200, 5120, "bf16", "fp32", False, "e4m3", True),
     (1184, 5120, "bf16", "bf16", True, "bf16", False), (1185, 2048, "fp16", None, True, "e4m3", False),
     (1400, 2560, "bf16", "bf16", False, "int8", False), (1201, 13312, "bf16", None, False, "int8", True),
-    (3000, 1000, "fp16", "bf16", False, "bf16", False)])
+    (3000, 1000, "fp16", "bf16", False, "bf16", False), (1191, 2051, "bf16", "bf16", False, "bf16", False),
+    (1300, 4125, "bf16", "fp32", False, "fp16", False), (1185, 2049, "fp16", None, False, "int8", False),
+    (2500, 2063, "fp32", "fp16", False, "e4m3", False), (40, 17, "bf16", "bf16", False, "bf16", False),
+    (33, 9, "fp16", "fp32", False, "int8", False), (700, 5, "bf16", "bf16", False, "e4m3", False)])
 def test_many_rows(m, k, xt, rt, signs, yt, grouped):
-    """Rows that come by copies issued ahead, several a block (and a width just under)."""
+    """Rows that come by copies issued ahead, several a block (and a width just
+    under), and rows that start anywhere in 16 bytes."""
     group = 0 if yt not in TOP else (128 if grouped else k)
     c = Norm(k + m, m, k, xt, rt, "bf16", signs, yt, group).run(guard=1)
     c.check()
@@ -168,6 +172,8 @@ def test_many_rows(m, k, xt, rt, signs, yt, grouped):
 def test_unaligned_and_no_weight(yt, group, signs):
     # one element past a 16-byte boundary, and no weight
     Norm(9, 3, 1024, "bf16", "fp16", None, signs, yt, group, by=1).run().check()
+    if not signs and group != 128:
+        Norm(9, 5, 1023, "bf16", "fp16", "fp32", signs, yt, group and 1023, by=3).run().check()
 
 
 @pytest.mark.parametrize("yt,group", [("bf16", 0), ("fp32", 0), ("int8", 640), ("e4m3", 128)])
