@@ -158,7 +158,10 @@ struct Q4DecodeParams {
 constexpr int kQ4DecBoxRows = 16;
 constexpr int kQ4DecBoxBytes = kQ4DecBoxRows * 128;
 // shared memory: rings | x planes [Gs][2][C][4] x 16 bytes | factors, sums [Gs][8 NT] each | barriers | partial sums
-constexpr int kQ4DecRingBytes = kQ4DecWarps * kQ4DecSlots * kQ4DecBoxBytes;
+// kb boxes (2 kb groups) a slot: two where x' is copied and leaves room, for half the
+// waits and scale loads a group (16 x 17408 x 5120 25.2 -> 24.1 us); one where the CTA
+// makes the planes itself, whose loads of x two would delay (1 x 6144 x 5120 6.6 -> 7.0)
+__host__ __device__ constexpr int q4_dec_ring_bytes(int kb) { return kQ4DecWarps * kQ4DecSlots * kb * kQ4DecBoxBytes; }
 __host__ __device__ constexpr int64_t q4_dec_x_bytes(int C, int Gs) { return int64_t(128) * C * Gs; }
 __host__ __device__ constexpr int64_t q4_dec_f_bytes(int C, int Gs) { return int64_t(64) * ((C + 7) / 8) * Gs; }
 __host__ __device__ constexpr int64_t q4_dec_part_bytes(int C, int rows, int Wk) { return int64_t(4) * Wk * C * rows; }
@@ -293,10 +296,11 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   return v;
 }
 
-// NT: column tiles of 8.
-template <int NT>
+// NT: column tiles of 8; KB: boxes of a slot.
+template <int NT, int KB>
 __global__ void __launch_bounds__(32 * kQ4DecWarps, 1)
     q4_decode_kernel(const __grid_constant__ CUtensorMap tm_w, const Q4DecodeParams p) {
+  constexpr int kSlot = KB * kQ4DecBoxBytes, kSG = 2 * KB;  // bytes and 128-groups of a slot
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int M = p.M, C = p.C, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -306,8 +310,8 @@ __global__ void __launch_bounds__(32 * kQ4DecWarps, 1)
   const int rank = p.S > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int cluster = static_cast<int>(blockIdx.x) / p.S, nclusters = static_cast<int>(gridDim.x) / p.S;
   const int G = p.K >> 7, G0 = rank * p.Gs, Gn = max(0, min(p.Gs, G - G0));
-  uint8_t* ring = smem + warp * kQ4DecSlots * kQ4DecBoxBytes;
-  uint4* xf = reinterpret_cast<uint4*>(smem + kQ4DecRingBytes);
+  uint8_t* ring = smem + warp * kQ4DecSlots * kSlot;
+  uint4* xf = reinterpret_cast<uint4*>(smem + q4_dec_ring_bytes(KB));
   float* xsg = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(xf) + q4_dec_x_bytes(C, p.Gs));
   int* xsum = reinterpret_cast<int*>(xsg + p.Gs * 8 * NT);
   uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(xsg) + q4_dec_f_bytes(C, p.Gs)) +
@@ -315,19 +319,21 @@ __global__ void __launch_bounds__(32 * kQ4DecWarps, 1)
   float* part = reinterpret_cast<float*>(smem + p.part_at);
 
   const int wt = warp % p.Wt, wk = warp / p.Wt;
-  const int nbox = (Gn + 1) >> 1;                                    // boxes of two groups in the slice
+  const int nbox = (Gn + kSG - 1) / kSG;  // slots' worth in the slice
   const int nb = wk < p.Wk && nbox > wk ? (nbox - wk + p.Wk - 1) / p.Wk : 0;  // this warp's, per row block
   const int mine = (p.nblocks - cluster + nclusters - 1) / nclusters;  // row blocks of this cluster
   const int total = mine * nb;
   const int R = p.Wt * p.rw;
-  const uint32_t bytes = static_cast<uint32_t>(p.rw) * 128u;
+  const uint32_t bytes = static_cast<uint32_t>(p.rw) * 128u * KB;
 
   // the producer's place: block and box index of the next box to fetch
   int fb = 0, fj = 0, fs = 0;
   auto fetch = [&]() {
     const int row = (cluster + fb * nclusters) * R + wt * p.rw;
     mbar_arrive_expect_tx(&bars[fs], bytes);
-    tma_load_2d(ring + fs * kQ4DecBoxBytes, &tm_w, (G0 + 2 * (wk + p.Wk * fj)) * 64, row, &bars[fs]);
+#pragma unroll
+    for (int b = 0; b < KB; ++b)
+      tma_load_2d(ring + fs * kSlot + b * kQ4DecBoxBytes, &tm_w, (G0 + kSG * (wk + p.Wk * fj) + 2 * b) * 64, row, &bars[fs]);
     if (++fj == nb) {
       fj = 0;
       ++fb;
@@ -340,17 +346,17 @@ __global__ void __launch_bounds__(32 * kQ4DecWarps, 1)
     for (int s = 0; s < kQ4DecSlots && s < total; ++s) fetch();  // weights do not wait for the previous kernel
   }
   // scales of this lane's rows (rho, rho + 8), fetched a box ahead
-  uint16_t sn[2][2];
+  uint16_t sn[kSG][2];
   auto load_scales = [&](int ib, int j) {
     const int64_t row = static_cast<int64_t>(cluster + ib * nclusters) * R + wt * p.rw + rho;
-    const int g = 2 * (wk + p.Wk * j);
+    const int g = kSG * (wk + p.Wk * j);
     const uint16_t* src = p.scales + row * G + G0 + g;
     const int left = static_cast<int>(min(p.N - row, static_cast<int64_t>(p.rw - rho)));  // rows from rho on
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      sn[0][h] = 8 * h < left ? __ldg(src + 8 * h * G) : uint16_t(0);
-      sn[1][h] = 8 * h < left && g + 1 < Gn ? __ldg(src + 8 * h * G + 1) : uint16_t(0);
-    }
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int gg = 0; gg < kSG; ++gg)
+        sn[gg][h] = 8 * h < left && g + gg < Gn ? __ldg(src + 8 * h * G + gg) : uint16_t(0);
   };
   if (nb > 0) load_scales(0, 0);
   pdl_launch_dependents();
@@ -396,18 +402,19 @@ __global__ void __launch_bounds__(32 * kQ4DecWarps, 1)
       for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
     if (nb > 0 && ib > 0) load_scales(ib, 0);
     for (int j = 0; j < nb && ok; ++j) {
-      float sc[2][2];
+      float sc[kSG][2];
 #pragma unroll
-      for (int h = 0; h < 4; ++h) sc[h & 1][h >> 1] = __half2float(__ushort_as_half(sn[h & 1][h >> 1]));
+      for (int h = 0; h < 2 * kSG; ++h) sc[h >> 1][h & 1] = __half2float(__ushort_as_half(sn[h >> 1][h & 1]));
       if (j + 1 < nb) load_scales(ib, j + 1);
       if (!__all_sync(0xffffffffu, mbar_wait(&bars[slot], phase, FAULT_WAIT_FULL))) {
         ok = false;
         break;
       }
-      const uint8_t* box = ring + slot * kQ4DecBoxBytes + rho * 128;
-      const int g0 = 2 * (wk + p.Wk * j);
+      const uint8_t* boxes = ring + slot * kSlot + rho * 128;
+      const int g0 = kSG * (wk + p.Wk * j);
 #pragma unroll
-      for (int gg = 0; gg < 2; ++gg) {
+      for (int gg = 0; gg < kSG; ++gg) {
+        const uint8_t* box = boxes + (gg >> 1) * kQ4DecBoxBytes;
         const int g = min(g0 + gg, Gn - 1);  // past an odd end: any x', the scales are zero
         const uint4* xg = xf + g * 8 * C + lane;
         uint4 b[NT][2];
@@ -421,7 +428,7 @@ __global__ void __launch_bounds__(32 * kQ4DecWarps, 1)
           d0[t] = *reinterpret_cast<const int2*>(xsum + g * 8 * NT + 8 * t + 2 * c);
           f[t] = *reinterpret_cast<const float2*>(xsg + g * 8 * NT + 8 * t + 2 * c);
         }
-        const int at = 16 * ((4 * gg + c) ^ rho);  // the 128-byte swizzle of a box row
+        const int at = 16 * ((4 * (gg & 1) + c) ^ rho);  // the 128-byte swizzle of a box row
         const uint4 lo = *reinterpret_cast<const uint4*>(box + at);
         const uint4 hi = *reinterpret_cast<const uint4*>(box + 1024 + at);
         int d[NT][4];

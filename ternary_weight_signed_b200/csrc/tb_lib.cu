@@ -1347,7 +1347,7 @@ tb_status run_q4_mid(const Q4Args& a, const DevInfo* d) {
 }
 
 struct Q4DecodePlan {
-  int NT, C, P, rw, nblocks, Wt, Wk, S, Gs, clusters, part_at;
+  int NT, KB, C, P, rw, nblocks, Wt, Wk, S, Gs, clusters, part_at;
   size_t smem;
 };
 
@@ -1375,27 +1375,34 @@ bool q4_decode_plan(int64_t N, int64_t K, int M, int P, bool copied, int sm_coun
       const int64_t nblocks = (N + static_cast<int64_t>(Wt) * rw - 1) / (static_cast<int64_t>(Wt) * rw);
       const int64_t part = q4_dec_part_bytes(C, kQ4DecBoxRows * Wt, Wk);
       const bool once = nblocks <= clusters;  // the partial sums then lie over x'
-      const int64_t smem = 1024 + kQ4DecRingBytes + (once ? std::max(x, part) : x + part);
-      if (smem > max_smem) continue;
-      const int64_t boxes = (Gs / 2 + Wk - 1) / Wk;
+      const int64_t rest = 1024 + (once ? std::max(x, part) : x + part);
+      const int KB = copied && rest + q4_dec_ring_bytes(2) <= max_smem ? 2 : 1, ring = q4_dec_ring_bytes(KB);
+      if (rest + ring > max_smem) continue;
+      const int64_t boxes = ((Gs + 2 * KB - 1) / (2 * KB) + Wk - 1) / Wk * KB;
       const int64_t cost =
           rounds * (boxes * 2 * (300 + 200 * NT) + 3000 + (S > 1 ? 2500 : 0)) + passes * (copied ? 60 : 1200);
       if (best >= 0 && cost >= best) continue;
       best = cost;
-      *out = Q4DecodePlan{NT, C, P, rw, static_cast<int>(nblocks), Wt, Wk, S, Gs, clusters,
-                          static_cast<int>(once ? kQ4DecRingBytes : kQ4DecRingBytes + x), static_cast<size_t>(smem)};
+      *out = Q4DecodePlan{NT, KB, C, P, rw, static_cast<int>(nblocks), Wt, Wk, S, Gs, clusters,
+                          static_cast<int>(once ? ring : ring + x), static_cast<size_t>(rest + ring)};
     }
   }
   return best >= 0;
 }
 
-template <int NT>
-tb_status launch_q4_decode(const CUtensorMap& tm, const Q4DecodeParams& p, const Q4DecodePlan& pl, const DevInfo* d,
+template <int NT, int KB>
+tb_status launch_q4_decode_kb(const CUtensorMap& tm, const Q4DecodeParams& p, const Q4DecodePlan& pl, const DevInfo* d,
                            cudaStream_t st) {
-  auto k = q4_decode_kernel<NT>;
+  auto k = q4_decode_kernel<NT, KB>;
   if (allow_smem(k, d) != TB_OK) return TB_ERR_CUDA;
   return launch_cluster(k, dim3(static_cast<unsigned>(pl.S * std::min(pl.clusters, pl.nblocks))), dim3(32 * kQ4DecWarps),
                         pl.smem, pl.S, st, tm, p);
+}
+
+template <int NT>
+tb_status launch_q4_decode(const CUtensorMap& tm, const Q4DecodeParams& p, const Q4DecodePlan& pl, const DevInfo* d,
+                           cudaStream_t st) {
+  return pl.KB == 2 ? launch_q4_decode_kb<NT, 2>(tm, p, pl, d, st) : launch_q4_decode_kb<NT, 1>(tm, p, pl, d, st);
 }
 
 tb_status run_q4_decode(const Q4Args& a, const DevInfo* d, const Q4DecodePlan& pl) {
