@@ -366,7 +366,12 @@ size_t tb_q4_linear_workspace(int64_t M, int64_t N, int64_t K);
  * workspace 16-byte aligned, signs 8 (else TB_ERR_ALIGN).
  * Accuracy: relative L2 error <= 2e-3 and per element <= 1e-2 * max|s| * 8 *
  * ||x_m||_2 before y's own rounding (the figures of tb_ternary_linear, w being
- * up to 8 s here). */
+ * up to 8 s here).  Up to 16 tokens the products are exact in a fixed-point x:
+ * an int8 x as it is, any other to 2^-22 (up to 5 tokens) or 2^-15 (6 to 16) of
+ * its 128-group's largest; past 16 tokens s q and x (scaled by a power of two a
+ * row) are rounded to fp16, 2^-11 relative.  Sums are fp32; the same call gives
+ * the same bits.  A NaN or an infinity in a row of x, or among its scales, makes
+ * that row of y NaN or infinite and touches no other. */
 tb_status tb_q4_linear(const void* x, tb_dtype xt, const float* x_scales, int64_t x_group,
                        const uint8_t* packed, const uint16_t* scales, int64_t M, int64_t N, int64_t K,
                        const int8_t* signs, void* y, tb_dtype yt, void* workspace, size_t ws_bytes,
@@ -381,9 +386,10 @@ tb_status tb_get_device_fault(uint32_t* code, int clear);
 
 /* Failure-detection test hook (no counterpart on the pages).  With stall != 0
  * the weight-copy producers of the one-token decode kernel and of the fp16
- * GEMM issue nothing, so every wait for those copies runs out: the kernel
- * records FAULT code 1 (a consumer gave up waiting for a stage) in the fault
- * word, returns without hanging and leaves its output incomplete.
+ * GEMMs (ternary and 4-bit, the latter from 17 tokens) issue nothing, so every
+ * wait for those copies runs out: the kernel records FAULT code 1 (a consumer
+ * gave up waiting for a stage) in the fault word, returns without hanging and
+ * leaves its output incomplete.
  * wait_limit_ns sets how long a bounded wait lasts (0 = the default 2 s), for
  * every kernel of the library on the current device.  Synchronous; call it
  * between kernels, with nothing of the library in flight, and call it again

@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(kMaxThreads, kMaxThreads <= 320 ? 2 : 1) rms_n
     const int64_t base = row * K;
     float v[NV][8];
     if constexpr (kMode == NORM_SHIFTED) {
-      cut = static_cast<int>(base & 7);
+      cut = p.vec ? static_cast<int>(base & 7) : 0;
       with_type(p.xt, [&](auto tx) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) norm_load_cut<decltype(tx)>(p.x, base, at(j), K, p.vec, v[j]);

@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kQmThreads, 1)
         f[j] = v.x, f[j + 1] = v.y, f[j + 2] = v.z, f[j + 3] = v.w;
       }
     }
-    const bool got = __all_sync(0xffffffffu, mbar_wait(accum, 0, FAULT_WAIT_EPILOGUE));
+    const bool got = __all_sync(0xffffffffu, mbar_wait(accum, 0, FAULT_WAIT_EPILOGUE, 4));
     if (ok && got) {
       tc_fence_after();
       uint32_t v[kCols];

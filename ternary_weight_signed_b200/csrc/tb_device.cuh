@@ -95,12 +95,12 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
 }
 
 // Waits for the phase with the given parity to complete.  Gives up after the
-// wait limit (2 s unless a test shortened it), records `fault` and returns
-// false.
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32_t fault) {
+// wait limit (2 s unless a test shortened it; `times` of it for a wait whose other
+// side may give up first and still signal), records `fault` and returns false.
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32_t fault, uint32_t times = 1) {
   if (mbar_try_wait(bar, parity)) return true;
   const unsigned long long t0 = global_ns();
-  const unsigned long long limit = wait_limit_ns();
+  const unsigned long long limit = wait_limit_ns() * times;
   for (;;) {
     if (mbar_try_wait(bar, parity)) return true;
     if (global_ns() - t0 > limit) {

@@ -1160,7 +1160,7 @@ tb_status run_norm_pieces(const NormParams& p, const DevInfo* d, cudaStream_t st
   // pieces of a thread: one where a row is alone on its SM (latency), else two, or
   // up to four when the rows come by bulk copies (more bytes in flight a thread,
   // fewer barriers a byte; without the copies four would spill)
-  const int pieces = (p.K + 7) / 8 + (kMode == NORM_SHIFTED ? 1 : 0);
+  const int pieces = (p.K + 7) / 8 + (kMode == NORM_SHIFTED && p.vec ? 1 : 0);
   const bool many = p.M > 2 * d->sm_count;
   int nv = 1;
   while (nv < 4 && (pieces > 1024 * nv || (many && pieces >= 256 * nv))) nv *= 2;
@@ -1725,8 +1725,8 @@ tb_status tb_rms_norm(const void* x, tb_dtype xt, const void* residual, void* re
   const DevInfo* d = nullptr;
   const tb_status st = current_device(&d);
   if (st != TB_OK) return st;
-  // (weights are read value by value where K % 8 != 0)
-  const bool vec = aligned(x, 16) && aligned(y, y8 ? 8 : 16) &&
+  // where K % 8 != 0 a row may touch one piece more, and the weights are read value by value
+  const bool vec = (K % 8 == 0 || K <= TB_RMS_NORM_MAX_K - 8) && aligned(x, 16) && aligned(y, y8 ? 8 : 16) &&
                    (residual == nullptr || (aligned(residual, 16) && aligned(residual_out, 16))) &&
                    (weight == nullptr || K % 8 != 0 || aligned(weight, 16));
   const NormParams p{x, residual, residual_out, weight, signs, y, y_scales, M, static_cast<int>(K),

@@ -116,7 +116,7 @@ class Norm:
 
 
 SIZES = [(1, 1), (1, 7), (3, 128), (2, 129), (5, 1000), (4, 1024), (1, 5120), (7, 2056), (2, 17408), (3, 8191), (2, 32768),
-         (300, 640)]
+         (9, 32767), (9, 32759), (9, 16383), (9, 8185), (300, 640)]
 
 
 @pytest.mark.parametrize("m,k", SIZES)

@@ -357,6 +357,41 @@ def test_norm_then_linear(m, yt, group):
     assert np.linalg.norm(got - dref) <= 0.15 * np.linalg.norm(dref)
 
 
+@pytest.mark.parametrize("m", [2, 9, 30, 140])
+@pytest.mark.parametrize("yt,group", [("int8", 256), ("int8", 128), ("e4m3", 256), ("e4m3", 128)])
+def test_a_row_without_numbers_through_both(m, yt, group):
+    """A NaN in a row of x reaches that row of y, and a row of zeros gives zeros."""
+    n, k = 70, 256
+    c = Linear(77, m, n, k, "bf16", 0, False, "fp32")
+    x = torch.randn(m, k, device=DEV).to(torch.bfloat16)
+    x[0, 3] = float("nan")
+    x[1] = 0.0
+    a = torch.empty(m, k, dtype=T[yt][1], device=DEV)
+    xs, y = torch.empty(m, k // group, device=DEV), torch.full((m, n), 77.0, device=DEV)
+    wsb = tb.tb_q4_linear_workspace(m, n, k)
+    ws = torch.empty(wsb, dtype=torch.uint8, device=DEV)
+    tb.tb_rms_norm(x, tb.TB_BF16, None, None, 0, None, 0, 1e-6, None, m, k, a, T[yt][0], xs, group)
+    tb.tb_q4_linear(a, T[yt][0], xs, group, c.packed, c.dscales, m, n, k, None, y, tb.TB_FP32, ws, wsb)
+    assert torch.isnan(y[0]).all() and not y[1].any() and torch.isfinite(y[1:]).all()
+
+
+@pytest.mark.parametrize("m,n,k", [(64, 3000, 1024), (20, 300, 2048), (200, 600, 1024)])
+def test_waits_run_out_and_the_next_call_is_right(m, n, k):
+    """With the copies of the weights held back (the library's test hook) every
+    wait for them runs out, the call returns and says so, and the next is right."""
+    c = Linear(n, m, n, k, "bf16", 0, False, "bf16")
+    tb.tb_get_device_fault(clear=True)
+    tb.tb_test_stall_copies(1, 20_000_000)
+    try:
+        c.run()
+        code = tb.tb_get_device_fault(clear=True)
+    finally:
+        tb.tb_test_stall_copies(0, 0)
+    assert code == 1, code
+    for _ in range(2):
+        c.run().check()
+
+
 @pytest.mark.parametrize("m", [1, 40])
 def test_norm_then_ternary_linear(m):
     """The norm with the rotation in front of the ternary layer (signs NULL there)
