@@ -5,8 +5,9 @@
 //   n_b <- H (d_b * n_b) / 32 per 1024-block (optional),
 //   y = n, or per group scale = max|n| / Q and y = round(n / scale).
 //
-// Bound by HBM past a few hundred rows, by the launch and two passes of latency
-// for one.  A row stays in registers between its one load and its one store: a
+// Bound by HBM past a few hundred rows (16384 x 5120, fp32 residual, e4m3 groups:
+// 148 us, 0.96 of the measured copy rate; rotated, 2048 x 5120: 20.2 us, by issue), by
+// the launch and two passes of latency for one (2.7 us).  A row stays in registers between its one load and its one store: a
 // thread holds NV pieces of 8 values (16-byte loads of 16-bit types), a block a
 // row, and the blocks walk the rows.  In the rotated kernel a warp holds a whole
 // 1024-block, so the transform needs no block-wide barrier: distances 1-4, 256 and

@@ -1,8 +1,8 @@
 // Linear layer with 4-bit g128 weights:
 //   y[m, n] = sum_g s[n, g] sum_{k in g} q[n, k] x'[m, k].
 //
-// Here: the activation prep (rotation, fp16 with a factor per token) that the
-// pair GEMM and the rotated decode read, and the decode kernel for few tokens.
+// Here: the activation prep of the tcgen05 kernels (q4_mid.cuh, gemm_pair.cuh) and
+// the decode kernel for up to 16 tokens with its own.
 #pragma once
 #include "gemm_pair.cuh"
 #include "norm.cuh"
@@ -118,9 +118,13 @@ __global__ void __launch_bounds__(1024)
 //     plus the bits of 1.5 2^23, which makes the integer sum a float's mantissa: one
 //     subtraction instead of a conversion.  The groups are added in fp32.
 //   * Measured on B200, cycles an MMA on one of the SM's four tensor pipes:
-//     m16n8k16 f16 15.4, m16n8k32 s8 15.8, m16n8k32 e4m3 35 (no pipe of its own).
-//     tcgen05.mma with 128 rows takes 47-56 cycles an SM for any N up to 64, K = 16:
-//     36 weights a cycle against 128 / (columns / 8) here.
+//     m16n8k16 f16 and m16n8k32 s8 8 with constant operands and 15-16 with ones that
+//     change, m16n8k32 e4m3 35 (no pipe of its own).  The f16 form unpacks a 16 x 128
+//     tile in 88 instructions, this one in 24 (1 x 17408 x 5120: 24.1 against 13.7 us
+//     when it replaced it).  tcgen05 wants the codes unpacked to 8 or 16 bits in tensor
+//     memory first; past 16 tokens that pays (q4_mid.cuh).
+//   * One token, 17408 x 5120: 11.3 us a call (0.63 of the measured HBM rate), of which
+//     5 us stream; 151936 x 5120: 78.5 us (0.79).
 //   * Each warp streams its own rows: boxes of up to 16 rows x 128 bytes (256
 //     codes) by TMA into a ring of its own, refilled by the warp itself, so no warp
 //     waits for another inside the loop.  K is spread over Wk of a CTA's warps

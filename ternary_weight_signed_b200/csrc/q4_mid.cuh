@@ -14,7 +14,9 @@
 //     barrier each adds its share of the tokens over the S CTAs in rank order
 //     (no atomics).
 // Bound: the copies of the codes and the L2 reads of x' by every tile (BT * K * 2
-// bytes a tile); the MMAs take 5.6 us of 17408 x 5120 at 64 tokens.
+// bytes a tile); the MMAs take 5.6 us of 17408 x 5120 at 64 tokens.  Measured with
+// the prep: 21.9 us at 32 tokens, 23.3 at 64, 26.2 at 128 (the pair GEMM: 34.7), held by
+// the round trip between the unpack warps and the MMAs.
 // The codes come in boxes of 128 rows x 128 bytes, two stages at a time: a TMA copy
 // of 64-byte rows runs at 2.6 TB/s over the device, one of 128-byte rows at 4 and
 // more (measured alone, launches included).
