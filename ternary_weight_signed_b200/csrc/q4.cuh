@@ -2,12 +2,12 @@
 // producer side, which folds the rotation into a dense matrix and rounds every
 // 128-group to q in -8..7 with s = fp16(fp32(max|w'| / 7)).
 //
-// The fold works in fp64 like prepare.cuh's (one warp per row and 1024-block): for
-// bf16 and fp16 input its sums are exact, so codes and scales do not depend on
-// summation order.  Without a fold the values are fp32 as they come.  17408 x 5120
+// The fold's sums are exact (fp32 slices for 16-bit input, else fp64 as in
+// prepare.cuh), so codes and scales do not depend on summation order.  Without a fold the values are fp32 as they come.  17408 x 5120
 // bf16 folded: about 390 us, by the latency of its fp64 sums at 16 warps an SM; 1024 x
 // 5120 fp32 unfolded: 8 us.
 #pragma once
+#include "norm.cuh"
 #include "prepare.cuh"
 #include "tb_device.cuh"
 
@@ -65,21 +65,13 @@ __device__ __forceinline__ uint32_t q4_code(float v, float inv, __half s, F&& ex
   return static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(q, -8.f), 7.f)) + 8);
 }
 
-// Folded: grid ceil(K / 1024) * ceil(N / kPwWarps) blocks, one warp per (row, block).
+// One (row, 1024-block) folded in fp64: any input.  xb: 512 doubles of the warp's own.
 template <typename TIn>
-__global__ void __launch_bounds__(32 * kPwWarps)
-    q4_fold_kernel(const TIn* __restrict__ w, const int8_t* __restrict__ signs, uint8_t* __restrict__ packed,
-                   uint16_t* __restrict__ scales, int64_t N, int K) {
-  __shared__ __align__(16) double xbuf[kPwWarps][512];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int nblk = K / kHB;
-  const int blk = static_cast<int>(blockIdx.x % nblk);
-  const int64_t row = static_cast<int64_t>(blockIdx.x / nblk) * kPwWarps + warp;
-  if (row >= N) return;  // a whole warp; nothing below synchronises beyond the warp
-  const int G = K >> 7;
-  const int64_t at = row * K + static_cast<int64_t>(blk) * kHB;
+__device__ __noinline__ void q4_fold_block_fp64(const TIn* __restrict__ w, const int8_t* __restrict__ signs,
+                                                uint8_t* __restrict__ packed, uint16_t* __restrict__ scales, int lane,
+                                                double* xb) {
   double v[32];
-  pw_load_folded<TIn>(w + at, signs + static_cast<int64_t>(blk) * kHB, xbuf[warp], lane, v);
+  pw_load_folded<TIn>(w, signs, xb, lane, v);
   double m = 0.0;
 #pragma unroll
   for (int i = 0; i < 32; ++i) m = fmax(m, fabs(v[i]));
@@ -91,8 +83,102 @@ __global__ void __launch_bounds__(32 * kPwWarps)
 #pragma unroll
   for (int i = 0; i < 32; ++i)
     wd[i >> 3] |= (sf > 0.f ? q4_code(static_cast<float>(v[i]), inv, s, [&] { return v[i]; }) : 8u) << (4 * (i & 7));
-  if ((lane & 3) == 0) scales[row * G + blk * 8 + (lane >> 2)] = __half_as_ushort(s);
-  *reinterpret_cast<uint4*>(packed + (at >> 1) + 16 * lane) = make_uint4(wd[0], wd[1], wd[2], wd[3]);
+  if ((lane & 3) == 0) scales[lane >> 2] = __half_as_ushort(s);
+  *reinterpret_cast<uint4*>(packed + 16 * lane) = make_uint4(wd[0], wd[1], wd[2], wd[3]);
+}
+
+// Folded: grid K / 1024 * ceil(N / kPwWarps) blocks, one warp per (row, block).
+//
+// 16-bit input is folded in fp32, exactly.  With the block scaled by a power of two
+// to |u| < 2, u = h + l with h a multiple of 2^-12 and l one of 2^-26, |l| <= 2^-13:
+// 1024 of either add up to less than 2^24 of their units, so every sum of the two
+// transforms is exact in fp32, and so is their sum in fp64.  A value that needs more
+// than the two slices (a bf16 below 2^-19 of 2, 3 blocks in 1000 of normal weights)
+// and fp32 input send the block to the fp64 fold.
+template <typename TIn>
+__global__ void __launch_bounds__(32 * kPwWarps, 2)
+    q4_fold_kernel(const TIn* __restrict__ w, const int8_t* __restrict__ signs, uint8_t* __restrict__ packed,
+                   uint16_t* __restrict__ scales, int64_t N, int K, bool vec) {
+  __shared__ __align__(16) float buf[kPwWarps][kNormRotFloats];  // (the fp64 fold takes 1024 of them)
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nblk = K / kHB;
+  const int blk = static_cast<int>(blockIdx.x % nblk);
+  const int64_t row = static_cast<int64_t>(blockIdx.x / nblk) * kPwWarps + warp;
+  if (row >= N) return;  // a whole warp; nothing below synchronises beyond the warp
+  const int64_t at = row * K + static_cast<int64_t>(blk) * kHB;
+  const TIn* src = w + at;
+  const int8_t* sg = signs + static_cast<int64_t>(blk) * kHB;
+  uint8_t* dst = packed + (at >> 1);
+  uint16_t* sdst = scales + at / 128;
+  if constexpr (sizeof(TIn) == 2) {
+    float h[4][8], l[4][8];
+    uint32_t mb = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int k = 256 * j + 8 * lane;
+      norm_load8<TIn>(src, k, vec, h[j]);
+      const uint2 s = *reinterpret_cast<const uint2*>(sg + k);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        h[j][e] = __uint_as_float(__float_as_uint(h[j][e]) ^ (((e < 4 ? s.x : s.y) << (24 - 8 * (e & 3))) & 0x80000000u));
+        mb = max(mb, abs_bits(h[j][e]));
+      }
+    }
+    mb = __reduce_max_sync(0xffffffffu, mb);
+    const int E = static_cast<int>(mb >> 23) - 127;  // 2^E <= largest < 2^(E+1)
+    bool fits = E >= -100 && E <= 100;
+    const float scale_in = __uint_as_float(static_cast<uint32_t>(127 - (fits ? E : 0)) << 23);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float u = h[j][e] * scale_in;
+        // adding 1.5 2^11 (2^-3) rounds to a multiple of 2^-12 (2^-26)
+        h[j][e] = __fsub_rn(__fadd_rn(u, 3072.f), 3072.f);
+        const float r = __fsub_rn(u, h[j][e]);
+        l[j][e] = __fsub_rn(__fadd_rn(r, 0.1875f), 0.1875f);
+        fits = fits && l[j][e] == r;
+      }
+    if (__all_sync(0xffffffffu, fits)) {
+      norm_fwht(h, buf[warp], lane);
+      norm_fwht(l, buf[warp], lane);
+      const float out = __uint_as_float(static_cast<uint32_t>(127 + E - 5) << 23);  // 2^E / 32
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        // the group's largest |w'|, exact: of the values whose fp32 sum is largest
+        float f[8], m = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          f[e] = h[j][e] + l[j][e];
+          m = fmaxf(m, fabsf(f[e]));
+        }
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        double top = 0.0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (fabsf(f[e]) == m) top = fmax(top, fabs(static_cast<double>(h[j][e]) + static_cast<double>(l[j][e])));
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const __half s = q4_scale(top * static_cast<double>(out));
+        const float sf = __half2float(s), inv = sf > 0.f ? 1.f / sf * out : 0.f;
+        uint32_t wd = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          wd |= (sf > 0.f ? q4_code(f[e], inv, s,
+                                    [&] {
+                                      return (static_cast<double>(h[j][e]) + static_cast<double>(l[j][e])) *
+                                             static_cast<double>(out);
+                                    })
+                          : 8u)
+                << (4 * e);
+        *reinterpret_cast<uint32_t*>(dst + 128 * j + 4 * lane) = wd;
+        if ((lane & 15) == 0) sdst[2 * j + (lane >> 4)] = __half_as_ushort(s);
+      }
+      return;
+    }
+  }
+  q4_fold_block_fp64<TIn>(src, sg, dst, sdst, lane, reinterpret_cast<double*>(buf[warp]));
 }
 
 // Not folded: every value is one of fp32, and a warp takes eight 128-groups of a

@@ -1785,7 +1785,7 @@ tb_status tb_q4_prepare_weights(const void* w, tb_dtype wt, const int8_t* signs,
 #define TB_Q4P(T)                                                                                             \
   do {                                                                                                        \
     if (signs != nullptr)                                                                                     \
-      q4_fold_kernel<<<grid, block, 0, s>>>(static_cast<const T*>(w), signs, packed, scales, N, k);           \
+      q4_fold_kernel<<<grid, block, 0, s>>>(static_cast<const T*>(w), signs, packed, scales, N, k, aligned(w, 16)); \
     else                                                                                                      \
       q4_round_kernel<<<grid, block, 0, s>>>(static_cast<const T*>(w), packed, scales, N, k, aligned(w, 16)); \
   } while (0)

@@ -85,6 +85,32 @@ def test_prepare_bitexact(n, k, folded, wt):
     assert np.array_equal(packed.cpu().numpy(), q4o.pack(q))
 
 
+@pytest.mark.parametrize("wt", ["bf16", "fp16"])
+@pytest.mark.parametrize("span", [0, 12, 17, 20, 26])
+def test_prepare_folded_values_of_many_sizes(wt, span):
+    """Blocks whose values span up to 2^span below their largest (short and long
+    slices of the exact sums), a block of one value, and blocks of zeros."""
+    n, k = 40, 2048
+    rng = np.random.default_rng(span)
+    v = rng.standard_normal((n, k)) * 2.0 ** -rng.uniform(0, max(span, 1e-9), (n, k)) * 0.05
+    v[1, :1024] = 0
+    v[2, 1024:2048] = 0
+    v[2, 1500] = 0.03
+    v[3] *= 1e-3
+    w = torch.from_numpy(v).to(T[wt][1])
+    signs = draw_signs(rng, k)
+    packed = torch.zeros(n, k // 2, dtype=torch.uint8, device=DEV)
+    scales = torch.zeros(n, k // 128, dtype=torch.float16, device=DEV)
+    for off in (0, 1):  # and from 4 bytes past a 16-byte boundary
+        buf = torch.empty(n * k + 2, dtype=w.dtype, device=DEV)
+        d = buf[2 * off:2 * off + n * k].view(n, k)
+        d.copy_(w)
+        tb.tb_q4_prepare_weights(d, T[wt][0], signs.to(DEV), n, k, packed, scales)
+        q, s = q4o.prepare_weights(w.double().numpy(), signs.numpy())
+        assert np.array_equal(scales.cpu().numpy().view(np.uint16), s.view(np.uint16))
+        assert np.array_equal(packed.cpu().numpy(), q4o.pack(q))
+
+
 @pytest.mark.parametrize("size", [1e9, 30000.0, 1e-6, 3e-7, 1e-9])
 def test_prepare_ends_of_the_scale(size):
     rng = np.random.default_rng(2)
