@@ -2,10 +2,11 @@
 // producer side, which folds the rotation into a dense matrix and rounds every
 // 128-group to q in -8..7 with s = fp16(fp32(max|w'| / 7)).
 //
-// The fold's sums are exact (fp32 slices for 16-bit input, else fp64 as in
-// prepare.cuh), so codes and scales do not depend on summation order.  Without a fold the values are fp32 as they come.  17408 x 5120
-// bf16 folded: about 390 us, by the latency of its fp64 sums at 16 warps an SM; 1024 x
-// 5120 fp32 unfolded: 8 us.
+// The fold's codes and scales are those of exact sums (fp32 with a bound on its error
+// where that decides them, else exact fp32 slices, else fp64), so they do not depend on
+// summation order.  Without a fold the values are fp32 as they come.  17408 x 5120 bf16
+// folded, with its unpacking: 294 us, bound by issue (412 us with all sums in fp64, 359
+// with all in exact slices); 1024 x 5120 fp32 unfolded: 8 us.
 #pragma once
 #include "norm.cuh"
 #include "prepare.cuh"
@@ -87,29 +88,18 @@ __device__ __noinline__ void q4_fold_block_fp64(const TIn* __restrict__ w, const
   *reinterpret_cast<uint4*>(packed + 16 * lane) = make_uint4(wd[0], wd[1], wd[2], wd[3]);
 }
 
-// Folded: grid K / 1024 * ceil(N / kPwWarps) blocks, one warp per (row, block).
+// One (row, 1024-block) folded exactly.
 //
-// 16-bit input is folded in fp32, exactly.  With the block scaled by a power of two
-// to |u| < 2, u = h + l with h a multiple of 2^-12 and l one of 2^-26, |l| <= 2^-13:
-// 1024 of either add up to less than 2^24 of their units, so every sum of the two
+// 16-bit input is folded in fp32.  With the block scaled by a power of two to
+// |u| < 2, u = h + l with h a multiple of 2^-12 and l one of 2^-26, |l| <= 2^-13: 1024
+// of either add up to less than 2^24 of their units, so every sum of the two
 // transforms is exact in fp32, and so is their sum in fp64.  A value that needs more
 // than the two slices (a bf16 below 2^-19 of 2, 3 blocks in 1000 of normal weights)
 // and fp32 input send the block to the fp64 fold.
 template <typename TIn>
-__global__ void __launch_bounds__(32 * kPwWarps, 2)
-    q4_fold_kernel(const TIn* __restrict__ w, const int8_t* __restrict__ signs, uint8_t* __restrict__ packed,
-                   uint16_t* __restrict__ scales, int64_t N, int K, bool vec) {
-  __shared__ __align__(16) float buf[kPwWarps][kNormRotFloats];  // (the fp64 fold takes 1024 of them)
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int nblk = K / kHB;
-  const int blk = static_cast<int>(blockIdx.x % nblk);
-  const int64_t row = static_cast<int64_t>(blockIdx.x / nblk) * kPwWarps + warp;
-  if (row >= N) return;  // a whole warp; nothing below synchronises beyond the warp
-  const int64_t at = row * K + static_cast<int64_t>(blk) * kHB;
-  const TIn* src = w + at;
-  const int8_t* sg = signs + static_cast<int64_t>(blk) * kHB;
-  uint8_t* dst = packed + (at >> 1);
-  uint16_t* sdst = scales + at / 128;
+__device__ __noinline__ void q4_fold_block(const TIn* __restrict__ src, const int8_t* __restrict__ sg,
+                                           uint8_t* __restrict__ dst, uint16_t* __restrict__ sdst, int lane, bool vec,
+                                           float* buf) {
   if constexpr (sizeof(TIn) == 2) {
     float h[4][8], l[4][8];
     uint32_t mb = 0;
@@ -140,8 +130,8 @@ __global__ void __launch_bounds__(32 * kPwWarps, 2)
         fits = fits && l[j][e] == r;
       }
     if (__all_sync(0xffffffffu, fits)) {
-      norm_fwht(h, buf[warp], lane);
-      norm_fwht(l, buf[warp], lane);
+      norm_fwht(h, buf, lane);
+      norm_fwht(l, buf, lane);
       const float out = __uint_as_float(static_cast<uint32_t>(127 + E - 5) << 23);  // 2^E / 32
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -178,7 +168,100 @@ __global__ void __launch_bounds__(32 * kPwWarps, 2)
       return;
     }
   }
-  q4_fold_block_fp64<TIn>(src, sg, dst, sdst, lane, reinterpret_cast<double*>(buf[warp]));
+  q4_fold_block_fp64<TIn>(src, sg, dst, sdst, lane, reinterpret_cast<double*>(buf));
+}
+
+// Folded: grid K / 1024 * N blocks of one warp (warps of one block would wait for those
+// of them that fold exactly).
+//
+// First a plain fp32 transform with a bound on its error: ten levels of sums of at
+// most U = sum |u| round by less than 10.1 2^-24 U in all.  Where neither a scale nor a
+// code can depend on that error (four blocks in five of normal weights), it is done; the
+// others are folded exactly.  Either way the bits are those of exact arithmetic.  294 us
+// with one warp a block, 367 with eight.
+template <typename TIn>
+__global__ void __launch_bounds__(32, 24)
+    q4_fold_kernel(const TIn* __restrict__ w, const int8_t* __restrict__ signs, uint8_t* __restrict__ packed,
+                   uint16_t* __restrict__ scales, int K, bool vec) {
+  __shared__ __align__(16) float buf[kNormRotFloats];  // (the fp64 fold takes 1024 of them)
+  const int lane = threadIdx.x;
+  const int nblk = K / kHB;
+  const int blk = static_cast<int>(blockIdx.x % nblk);
+  const int64_t row = blockIdx.x / nblk;
+  const int64_t at = row * K + static_cast<int64_t>(blk) * kHB;
+  const TIn* src = w + at;
+  const int8_t* sg = signs + static_cast<int64_t>(blk) * kHB;
+  uint8_t* dst = packed + (at >> 1);
+  uint16_t* sdst = scales + at / 128;
+  float v[4][8], sum = 0.f;
+  uint32_t mb = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int k = 256 * j + 8 * lane;
+    norm_load8<TIn>(src, k, vec, v[j]);
+    const uint2 s = *reinterpret_cast<const uint2*>(sg + k);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      v[j][e] = __uint_as_float(__float_as_uint(v[j][e]) ^ (((e < 4 ? s.x : s.y) << (24 - 8 * (e & 3))) & 0x80000000u));
+      mb = max(mb, abs_bits(v[j][e]));
+      sum += fabsf(v[j][e]);
+    }
+  }
+  mb = __reduce_max_sync(0xffffffffu, mb);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  // |w'| stays far from the ends of fp32 (an empty or a wild block is folded exactly)
+  bool sure = mb > (27u << 23) && mb < (227u << 23);
+  norm_fwht(v, buf, lane);
+  const float err = sum * 6.03e-7f;  // 10.1 2^-24, with room for the rounding of the sum itself
+  float m[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    m[j] = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m[j] = fmaxf(m[j], fabsf(v[j][e]));
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], o));
+  }
+  // lane g < 8 takes the scale of group g (piece g / 2, half g % 2); it is sure where
+  // both ends of the interval round to it
+  float mine = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float o = __shfl_sync(0xffffffffu, m[j], 16 * (lane & 1));
+    if ((lane >> 1) == j) mine = o;
+  }
+  const double hi = (static_cast<double>(mine) + static_cast<double>(err)) * 0.03125;
+  const double lo = (static_cast<double>(mine) - static_cast<double>(err)) * 0.03125;
+  const __half s_hi = q4_scale(hi);
+  const float sf = __half2float(s_hi);
+  if (lane < 8)
+    sure = sure && lo > 0.0 && __half_as_ushort(q4_scale(lo)) == __half_as_ushort(s_hi) && sf >= 6.2e-5f && sf < kQ4MaxScale;
+  const float inv_mine = 0.03125f / sf;
+  uint32_t wd[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float inv = __shfl_sync(0xffffffffu, inv_mine, 2 * j + (lane >> 4));
+    // |r| <= 7.01: no code is clipped.  r is off by err inv and three roundings
+    const float edge = 0.5f - (err * inv * 1.01f + 2e-6f);
+    uint32_t acc = 0x88888888u;
+    float worst = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float q = fmaf(v[j][e], inv, 12582912.f);  // the nearest integer in the mantissa
+      worst = fmaxf(worst, fabsf(v[j][e] * inv - (q - 12582912.f)));
+      acc += (__float_as_uint(q) - 0x4B400000u) << (4 * e);
+    }
+    wd[j] = acc;
+    sure = sure && worst < edge;
+  }
+  if (!__all_sync(0xffffffffu, sure)) {
+    q4_fold_block<TIn>(src, sg, dst, sdst, lane, vec, buf);
+    return;
+  }
+  if (lane < 8) sdst[lane] = __half_as_ushort(s_hi);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) *reinterpret_cast<uint32_t*>(dst + 128 * j + 4 * lane) = wd[j];
 }
 
 // Not folded: every value is one of fp32, and a warp takes eight 128-groups of a

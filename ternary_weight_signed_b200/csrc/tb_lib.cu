@@ -1773,19 +1773,19 @@ tb_status tb_q4_prepare_weights(const void* w, tb_dtype wt, const int8_t* signs,
   if (!is_float_dtype(wt)) return TB_ERR_DTYPE;
   if (!q4_sizes_ok(1, N, K) || (signs != nullptr && K % 1024 != 0)) return TB_ERR_SHAPE;
   const int64_t blocks = (K + kHB - 1) / kHB * ((N + kPwWarps - 1) / kPwWarps);
-  if (blocks > kMaxDim) return TB_ERR_SHAPE;
+  if (blocks > kMaxDim || (signs != nullptr && K / kHB * N > kMaxDim)) return TB_ERR_SHAPE;
   if (!aligned(w, 4) || !aligned(packed, 16) || !aligned(scales, 2) || (signs != nullptr && !aligned(signs, 8)))
     return TB_ERR_ALIGN;
   const DevInfo* d = nullptr;
   const tb_status st = current_device(&d);
   if (st != TB_OK) return st;
   const cudaStream_t s = as_stream(stream);
-  const unsigned grid = static_cast<unsigned>(blocks);
+  const unsigned grid = static_cast<unsigned>(blocks), fold_grid = static_cast<unsigned>(K / kHB * N);
   const int block = 32 * kPwWarps, k = static_cast<int>(K);
 #define TB_Q4P(T)                                                                                             \
   do {                                                                                                        \
     if (signs != nullptr)                                                                                     \
-      q4_fold_kernel<<<grid, block, 0, s>>>(static_cast<const T*>(w), signs, packed, scales, N, k, aligned(w, 16)); \
+      q4_fold_kernel<<<fold_grid, 32, 0, s>>>(static_cast<const T*>(w), signs, packed, scales, k, aligned(w, 16)); \
     else                                                                                                      \
       q4_round_kernel<<<grid, block, 0, s>>>(static_cast<const T*>(w), packed, scales, N, k, aligned(w, 16)); \
   } while (0)

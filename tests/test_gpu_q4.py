@@ -111,6 +111,30 @@ def test_prepare_folded_values_of_many_sizes(wt, span):
         assert np.array_equal(packed.cpu().numpy(), q4o.pack(q))
 
 
+@pytest.mark.parametrize("wt", ["bf16", "fp16", "fp32"])
+def test_prepare_folded_ties(wt):
+    """Two values a and b in a block fold to |a +- b| / 32 everywhere: (21, 7) puts the
+    scale on an fp16 number and half the codes on q + 1/2, (7 2^11, 7) the scale
+    halfway between two fp16 numbers."""
+    n, k = 16, 2048
+    rng = np.random.default_rng(7)
+    v = np.zeros((n, k))
+    for i in range(n):
+        for blk in range(2):
+            at = 1024 * blk + rng.choice(1024, 2, replace=False)
+            pair = ((21.0, 7.0), (7.0 * 2 ** 11, 7.0))[i % 2]
+            v[i, at] = np.array(pair) * rng.choice([-1.0, 1.0], 2) * 2.0 ** -int(rng.integers(2, 10))
+    w = torch.from_numpy(v).to(T[wt][1])
+    assert np.array_equal(w.double().numpy(), v)
+    signs = draw_signs(rng, k)
+    packed = torch.zeros(n, k // 2, dtype=torch.uint8, device=DEV)
+    scales = torch.zeros(n, k // 128, dtype=torch.float16, device=DEV)
+    tb.tb_q4_prepare_weights(w.to(DEV), T[wt][0], signs.to(DEV), n, k, packed, scales)
+    q, s = q4o.prepare_weights(v, signs.numpy())
+    assert np.array_equal(scales.cpu().numpy().view(np.uint16), s.view(np.uint16))
+    assert np.array_equal(packed.cpu().numpy(), q4o.pack(q))
+
+
 @pytest.mark.parametrize("size", [1e9, 30000.0, 1e-6, 3e-7, 1e-9])
 def test_prepare_ends_of_the_scale(size):
     rng = np.random.default_rng(2)
