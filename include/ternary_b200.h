@@ -342,9 +342,10 @@ tb_status tb_q4_unpack(const uint8_t* packed, int64_t N, int64_t K, int8_t* code
  * aligned), folded with the rotation of `signs` (as in tb_prepare_weights;
  * needs K % 1024 == 0) or, signs NULL, taken as it is (K % 128 == 0), rounded
  * per 128-group: s = fp16(fp32(max|w'| / 7)), at most 8188;
- * q = clip(rint(w' / s), -8, 7) (halves to even), 0 where s = 0.  Computed in
- * fp64, with the exactness of tb_prepare_weights.  packed 16-byte aligned;
- * packed and scales are written in full. */
+ * q = clip(rint(w' / s), -8, 7) (halves to even), 0 where s = 0.  Codes and
+ * scales are those of fp64 sums, with the exactness of tb_prepare_weights.
+ * packed 16-byte aligned; packed and scales are written in full.  Folded, N K is
+ * at most 1024 (2^31 - 1), else TB_ERR_SHAPE. */
 tb_status tb_q4_prepare_weights(const void* w, tb_dtype wt, const int8_t* signs, int64_t N, int64_t K,
                                 uint8_t* packed, uint16_t* scales, void* stream);
 
