@@ -5,7 +5,7 @@
 // The fold's codes and scales are those of exact sums (fp32 with a bound on its error
 // where that decides them, else exact fp32 slices, else fp64), so they do not depend on
 // summation order.  Without a fold the values are fp32 as they come.  17408 x 5120 bf16
-// folded, with its unpacking: 294 us, bound by issue (412 us with all sums in fp64, 359
+// folded, with its unpacking: 260 us (412 us with all sums in fp64, 359
 // with all in exact slices); 1024 x 5120 fp32 unfolded: 8 us.
 #pragma once
 #include "norm.cuh"
@@ -177,10 +177,13 @@ __device__ __noinline__ void q4_fold_block(const TIn* __restrict__ src, const in
 // First a plain fp32 transform with a bound on its error: ten levels of sums of at
 // most U = sum |u| round by less than 10.1 2^-24 U in all.  Where neither a scale nor a
 // code can depend on that error (four blocks in five of normal weights), it is done; the
-// others are folded exactly.  Either way the bits are those of exact arithmetic.  294 us
-// with one warp a block, 367 with eight.
+// others are folded exactly.  Either way the bits are those of exact arithmetic.
+//
+// Bound by instruction fetch (straight-line code, each warp at another place in it) and
+// latency, so the most blocks an SM holds: 32 of 64 registers 260 us, 24 of 80 294, 16
+// of 128 392; two warps a block 275, four 303, eight 367.
 template <typename TIn>
-__global__ void __launch_bounds__(32, 24)
+__global__ void __launch_bounds__(32, 32)
     q4_fold_kernel(const TIn* __restrict__ w, const int8_t* __restrict__ signs, uint8_t* __restrict__ packed,
                    uint16_t* __restrict__ scales, int K, bool vec) {
   __shared__ __align__(16) float buf[kNormRotFloats];  // (the fp64 fold takes 1024 of them)
