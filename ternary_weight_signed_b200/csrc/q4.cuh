@@ -124,7 +124,7 @@ __device__ __noinline__ void q4_fold_block(const TIn* __restrict__ src, const in
       for (int e = 0; e < 8; ++e) {
         const float u = h[j][e] * scale_in;
         // adding 1.5 2^11 (2^-3) rounds to a multiple of 2^-12 (2^-26)
-        h[j][e] = __fsub_rn(__fadd_rn(u, 3072.f), 3072.f);
+        h[j][e] = __fsub_rn(__fadd_rn(u, 0x1.8p11f), 0x1.8p11f);
         const float r = __fsub_rn(u, h[j][e]);
         l[j][e] = __fsub_rn(__fadd_rn(r, 0.1875f), 0.1875f);
         fits = fits && l[j][e] == r;
