@@ -56,7 +56,8 @@ struct NormParams {
   int group;  // 0: floating output
   int xt, rt, wt, yt;
   float eps;
-  bool vec;  // every pointer that is read or written in pieces starts on 16 bytes
+  bool vec;    // every pointer that is read or written in pieces starts on 16 bytes
+  bool stall;  // failure-detection test: no copies
 };
 
 // Largest absolute value as its fp32 bits: NaN above infinity above the rest.
@@ -74,14 +75,22 @@ struct BlockReduce {
     set ^= 32;
     return red + set;
   }
-  __device__ __forceinline__ float sum(float v) {
+  // kAny: and whether `any` holds for one of the threads, in every thread's `any`.
+  template <bool kAny = false>
+  __device__ __forceinline__ float sum(float v, bool* any = nullptr) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     const int nw = blockDim.x >> 5, lane = threadIdx.x & 31;
-    if (nw == 1) return v;
+    if (nw == 1) {
+      if constexpr (kAny) *any = __any_sync(0xffffffffu, *any);
+      return v;
+    }
     uint32_t* r = next();
     if (lane == 0) r[threadIdx.x >> 5] = __float_as_uint(v);
-    __syncthreads();
+    if constexpr (kAny)
+      *any = __syncthreads_or(*any);
+    else
+      __syncthreads();
     v = lane < nw ? __uint_as_float(r[lane]) : 0.f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -286,17 +295,18 @@ __device__ __forceinline__ void norm_weight8(const NormParams& p, int k, float (
 }
 
 // kBulk: the rows come through shared memory, each by one or two bulk copies
-// issued kNormStages rows ahead (one is enough beside three to six blocks on an
-// SM; two leave room for fewer blocks: 170 against 149 us for 16384 x 5120), so that the copies of the next rows run while a
-// row is reduced, rotated and stored, and the weights (with the signs) lie there
-// too; for many rows (16-byte accesses only).
-constexpr int kNormStages = 1;
+// issued a row ahead (enough beside three to six blocks on an SM; two rows ahead
+// leave room for fewer blocks: 170 against 149 us for 16384 x 5120), so that the
+// copies of the next row run while a row is reduced, rotated and stored, and the
+// weights (with the signs) lie there too; for many rows (16-byte accesses only).
+// A block whose wait for a row gives up asks for no further row: after the row's
+// barrier all its threads leave, the first once its copy has landed.
 
 template <int NV, int kMode, int kMaxThreads, bool kBulk>
 __global__ void __launch_bounds__(kMaxThreads, kMaxThreads <= 320 ? 2 : 1) rms_norm_kernel(const NormParams p) {
   extern __shared__ __align__(16) float norm_smem[];
   __shared__ uint32_t red[64];
-  __shared__ uint64_t bars[kNormStages];
+  __shared__ uint64_t bar;
   pdl_launch_dependents();
   const int tid = threadIdx.x, T = blockDim.x, warp = tid >> 5, lane = tid & 31, K = p.K;
   BlockReduce reduce{red, 0};
@@ -307,18 +317,18 @@ __global__ void __launch_bounds__(kMaxThreads, kMaxThreads <= 320 ? 2 : 1) rms_n
   auto in = [&](int j) { return kMode == NORM_ROTATED || at(j) < K; };
   uint8_t* weights = reinterpret_cast<uint8_t*>(norm_smem + (kMode == NORM_ROTATED ? (T >> 5) * kNormRotFloats : 0));
   const int w_size = p.wt == DT_FP32 ? 4 : 2;
-  uint8_t* stages = weights + K * w_size;
+  uint8_t* stage = weights + K * w_size;
   const uint32_t x_bytes = static_cast<uint32_t>(K) * (p.xt == DT_FP32 ? 4 : 2);
   const uint32_t r_bytes = p.residual == nullptr ? 0u : static_cast<uint32_t>(K) * (p.rt == DT_FP32 ? 4 : 2);
-  auto fetch = [&](int64_t row, int s) {
-    uint8_t* dst = stages + s * (x_bytes + r_bytes);
-    mbar_arrive_expect_tx(&bars[s], x_bytes + r_bytes);
-    bulk_load(dst, static_cast<const uint8_t*>(p.x) + row * x_bytes, x_bytes, &bars[s]);
-    if (r_bytes != 0) bulk_load(dst + x_bytes, static_cast<const uint8_t*>(p.residual) + row * r_bytes, r_bytes, &bars[s]);
+  auto fetch = [&](int64_t row) {
+    if (p.stall || row >= p.M) return;
+    mbar_arrive_expect_tx(&bar, x_bytes + r_bytes);
+    bulk_load(stage, static_cast<const uint8_t*>(p.x) + row * x_bytes, x_bytes, &bar);
+    if (r_bytes != 0) bulk_load(stage + x_bytes, static_cast<const uint8_t*>(p.residual) + row * r_bytes, r_bytes, &bar);
   };
   if constexpr (kBulk) {
     if (tid == 0) {
-      for (int s = 0; s < kNormStages; ++s) mbar_init(&bars[s], 1);
+      mbar_init(&bar, 1);
       fence_mbar_init();
     }
 #pragma unroll
@@ -334,19 +344,13 @@ __global__ void __launch_bounds__(kMaxThreads, kMaxThreads <= 320 ? 2 : 1) rms_n
   }
   pdl_wait();
   if constexpr (kBulk) {
-    if (tid == 0) {
-      for (int s = 0; s < kNormStages; ++s) {
-        const int64_t row = blockIdx.x + static_cast<int64_t>(s) * gridDim.x;
-        if (row < p.M) fetch(row, s);
-      }
-    }
+    if (tid == 0) fetch(blockIdx.x);
   }
-  bool ok = true;
-  int stage = 0;
   uint32_t phase = 0;
   for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x) {
     const int64_t base = row * K;
     float v[NV][8];
+    bool gave_up = false;
     if constexpr (kMode == NORM_SHIFTED) {
       cut = p.vec ? static_cast<int>(base & 7) : 0;
       with_type(p.xt, [&](auto tx) {
@@ -368,10 +372,8 @@ __global__ void __launch_bounds__(kMaxThreads, kMaxThreads <= 320 ? 2 : 1) rms_n
         });
       }
     } else {
-      // after a wait that gave up the rows are wrong and the fault word says so
-      if constexpr (kBulk) ok = ok && mbar_wait(&bars[stage], phase, FAULT_WAIT_FULL);
-      const uint8_t* st = stages + stage * (x_bytes + r_bytes);
-      const void* xp = kBulk ? static_cast<const void*>(st) : p.x;
+      if constexpr (kBulk) gave_up = !mbar_wait(&bar, phase, FAULT_WAIT_FULL);
+      const void* xp = kBulk ? static_cast<const void*>(stage) : p.x;
       const int64_t xbase = kBulk ? 0 : base;
       const bool vec = kBulk || p.vec;
       with_type(p.xt, [&](auto tx) {
@@ -386,13 +388,13 @@ __global__ void __launch_bounds__(kMaxThreads, kMaxThreads <= 320 ? 2 : 1) rms_n
         }
       });
       if (p.residual != nullptr) {
-        const void* rp = kBulk ? static_cast<const void*>(st + x_bytes) : p.residual;
+        const void* rp = kBulk ? static_cast<const void*>(stage + x_bytes) : p.residual;
         with_type(p.rt, [&](auto tr) {
           auto add = [&](int j, const float (&r)[8]) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[j][e] += r[e];
             norm_round8<decltype(tr)>(v[j]);
-            norm_store8<decltype(tr)>(p.residual_out, base + at(j), vec, v[j]);
+            if (!gave_up) norm_store8<decltype(tr)>(p.residual_out, base + at(j), vec, v[j]);
           };
           if constexpr (kBulk) {
 #pragma unroll
@@ -419,15 +421,15 @@ __global__ void __launch_bounds__(kMaxThreads, kMaxThreads <= 320 ? 2 : 1) rms_n
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = fmaf(v[j][e], v[j][e], ss);
-    ss = reduce.sum(ss);
+    ss = reduce.sum<kBulk>(ss, &gave_up);
     if constexpr (kBulk) {
-      // every thread has its values in registers: the stage takes a later row
-      if (tid == 0 && row + static_cast<int64_t>(kNormStages) * gridDim.x < p.M)
-        fetch(row + static_cast<int64_t>(kNormStages) * gridDim.x, stage);
-      if (++stage == kNormStages) {
-        stage = 0;
-        phase ^= 1u;
+      if (gave_up) {
+        if (tid == 0 && !p.stall) mbar_wait(&bar, phase, FAULT_WAIT_FULL);
+        return;
       }
+      // every thread has its values in registers: the stage takes the next row
+      if (tid == 0) fetch(row + gridDim.x);
+      phase ^= 1u;
     }
     float inv;
     if (ss < 1e30f && ss > 1e-20f) {

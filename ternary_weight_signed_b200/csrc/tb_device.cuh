@@ -28,9 +28,10 @@ constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // 2 s
 __device__ uint32_t g_fault = 0;
 
 // Failure-detection test hook (tb_test_stall_copies): while bit 0 is set, the
-// TMA producers of the one-token decode and of the fp16 GEMM issue no weight
+// TMA producers of the one-token decode and of the fp16 GEMMs issue no weight
 // copies, so every wait for them runs out after g_wait_limit_ns.  Both words
-// are only ever written by the host between kernels.
+// are only ever written by the host between kernels.  (Kernels that could not
+// hide the read of the word get it as an argument.)
 __device__ uint32_t g_test_stall = 0;
 __device__ unsigned long long g_wait_limit_ns = kWaitLimitNs;
 

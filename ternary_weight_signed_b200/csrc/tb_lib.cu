@@ -7,6 +7,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <mutex>
 #include <unordered_set>
@@ -40,6 +41,7 @@ struct DevInfo {
   int sm_count = 0;
   int max_smem_optin = 0;
   int cc_major = 0;
+  std::atomic<bool> stall{false};  // set by tb_test_stall_copies
 };
 
 std::mutex g_mu;
@@ -1151,7 +1153,7 @@ bool norm_bulk(const NormParams& p, const DevInfo* d, size_t smem) {
 }
 
 size_t norm_stage_bytes(const NormParams& p) {
-  return (p.wt == TB_FP32 ? 4 : 2) * static_cast<size_t>(p.K) + kNormStages * static_cast<size_t>(p.K) *
+  return (p.wt == TB_FP32 ? 4 : 2) * static_cast<size_t>(p.K) + static_cast<size_t>(p.K) *
          ((p.xt == TB_FP32 ? 4 : 2) + (p.residual == nullptr ? 0 : (p.rt == TB_FP32 ? 4 : 2)));
 }
 
@@ -1730,7 +1732,8 @@ tb_status tb_rms_norm(const void* x, tb_dtype xt, const void* residual, void* re
                    (residual == nullptr || (aligned(residual, 16) && aligned(residual_out, 16))) &&
                    (weight == nullptr || K % 8 != 0 || aligned(weight, 16));
   const NormParams p{x, residual, residual_out, weight, signs, y, y_scales, M, static_cast<int>(K),
-                     static_cast<int>(scale_group), xt, rt, weight == nullptr ? TB_BF16 : wt, yt, eps, vec};
+                     static_cast<int>(scale_group), xt, rt, weight == nullptr ? TB_BF16 : wt, yt, eps, vec,
+                     d->stall.load(std::memory_order_relaxed)};
   return run_norm(p, d, as_stream(stream));
 }
 
@@ -1823,6 +1826,12 @@ tb_status tb_test_stall_copies(uint32_t stall, uint64_t wait_limit_ns) {
     cudaGetLastError();
     return TB_ERR_CUDA;
   }
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return TB_ERR_CUDA;
+  }
+  g_dev[dev].stall.store(v != 0);
   return TB_OK;
 }
 

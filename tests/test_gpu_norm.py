@@ -284,3 +284,25 @@ def test_streams_graphs_and_repeats():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(c.y.view(torch.uint8), want[0].view(torch.uint8)) and torch.equal(c.ro, want[2])
+
+
+@pytest.mark.parametrize("m,k,signs,rt,yt,group", [(2400, 1024, True, "bf16", "bf16", 0), (1300, 5120, False, "fp32", "e4m3", 128),
+                                                   (1300, 13312, False, None, "int8", 13312), (1200, 1032, False, "bf16", "fp16", 0)])
+def test_waits_run_out_and_the_next_call_is_right(m, k, signs, rt, yt, group):
+    """With the copies of the rows held back (the library's test hook) every wait
+    for them runs out, the call returns and says so without a value written, and the
+    next is right."""
+    c = Norm(k + m, m, k, "bf16", rt, "bf16", signs, yt, group)
+    tb.tb_get_device_fault(clear=True)
+    tb.tb_test_stall_copies(1, 20_000_000)
+    try:
+        c.run()
+        code = tb.tb_get_device_fault(clear=True)
+    finally:
+        tb.tb_test_stall_copies(0, 0)
+    assert code == 1, code
+    assert (c.y.float() == torch.tensor(77.0).to(T[yt][1]).float().item()).all()
+    for t in (c.ro, c.s):
+        assert t is None or (t == 77.0).all()
+    for _ in range(2):
+        c.run().check()
