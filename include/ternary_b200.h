@@ -387,11 +387,12 @@ tb_status tb_get_device_fault(uint32_t* code, int clear);
 
 /* Failure-detection test hook (no counterpart on the pages).  With stall != 0
  * the weight-copy producers of the one-token decode kernel and of the fp16
- * GEMMs (ternary and 4-bit, the latter from 17 tokens) issue nothing, and
- * neither do the row copies of tb_rms_norm (many rows), so every wait for those
- * copies runs out: the kernel records FAULT code 1 (a consumer gave up waiting
- * for a stage) in the fault word, returns without hanging and leaves its output
- * incomplete.  (A captured tb_rms_norm keeps the setting it was captured with.)
+ * GEMMs (ternary and 4-bit) issue nothing, and neither do those of the 4-bit
+ * decode kernel and the row copies of tb_rms_norm (many rows), so every wait for
+ * those copies runs out: the kernel records FAULT code 1 (a consumer gave up
+ * waiting for a stage) in the fault word, returns without hanging and leaves its
+ * output incomplete.  (The latter two, captured into a graph, keep the setting
+ * that they were captured with.)
  * wait_limit_ns sets how long a bounded wait lasts (0 = the default 2 s), for
  * every kernel of the library on the current device.  Synchronous; call it
  * between kernels, with nothing of the library in flight, and call it again

@@ -157,15 +157,19 @@ struct Q4DecodeParams {
   int Wt, Wk;       // row classes x K classes of a CTA's warps
   int S, Gs;        // cluster size, 128-groups of a CTA's K slice (even)
   int part_at;      // byte offset of the partial sums in shared memory
+  bool stall;       // failure-detection test: no copies
 };
 
 constexpr int kQ4DecBoxRows = 16;
 constexpr int kQ4DecBoxBytes = kQ4DecBoxRows * 128;
-// shared memory: rings | x planes [Gs][2][C][4] x 16 bytes | factors, sums [Gs][8 NT] each | barriers | partial sums
+// shared memory: rings | barriers | x planes [Gs][2][C][4] x 16 bytes | factors, sums [Gs][8 NT] each | partial sums
+// (these over x where a CTA has one row block; rings and barriers are never written over:
+// copies may be in flight after a wait that gave up)
 // kb boxes (2 kb groups) a slot: two where x' is copied and leaves room, for half the
 // waits and scale loads a group (16 x 17408 x 5120 25.2 -> 24.1 us); one where the CTA
 // makes the planes itself, whose loads of x two would delay (1 x 6144 x 5120 6.6 -> 7.0)
 __host__ __device__ constexpr int q4_dec_ring_bytes(int kb) { return kQ4DecWarps * kQ4DecSlots * kb * kQ4DecBoxBytes; }
+constexpr int kQ4DecBarBytes = 8 * kQ4DecWarps * kQ4DecSlots;
 __host__ __device__ constexpr int64_t q4_dec_x_bytes(int C, int Gs) { return int64_t(128) * C * Gs; }
 __host__ __device__ constexpr int64_t q4_dec_f_bytes(int C, int Gs) { return int64_t(64) * ((C + 7) / 8) * Gs; }
 __host__ __device__ constexpr int64_t q4_dec_part_bytes(int C, int rows, int Wk) { return int64_t(4) * Wk * C * rows; }
@@ -315,11 +319,10 @@ __global__ void __launch_bounds__(32 * kQ4DecWarps, 1)
   const int cluster = static_cast<int>(blockIdx.x) / p.S, nclusters = static_cast<int>(gridDim.x) / p.S;
   const int G = p.K >> 7, G0 = rank * p.Gs, Gn = max(0, min(p.Gs, G - G0));
   uint8_t* ring = smem + warp * kQ4DecSlots * kSlot;
-  uint4* xf = reinterpret_cast<uint4*>(smem + q4_dec_ring_bytes(KB));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + q4_dec_ring_bytes(KB)) + warp * kQ4DecSlots;
+  uint4* xf = reinterpret_cast<uint4*>(smem + q4_dec_ring_bytes(KB) + kQ4DecBarBytes);
   float* xsg = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(xf) + q4_dec_x_bytes(C, p.Gs));
   int* xsum = reinterpret_cast<int*>(xsg + p.Gs * 8 * NT);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(xsg) + q4_dec_f_bytes(C, p.Gs)) +
-                   warp * kQ4DecSlots;
   float* part = reinterpret_cast<float*>(smem + p.part_at);
 
   const int wt = warp % p.Wt, wk = warp / p.Wt;
@@ -333,6 +336,7 @@ __global__ void __launch_bounds__(32 * kQ4DecWarps, 1)
   // the producer's place: block and box index of the next box to fetch
   int fb = 0, fj = 0, fs = 0;
   auto fetch = [&]() {
+    if (p.stall) return;
     const int row = (cluster + fb * nclusters) * R + wt * p.rw;
     mbar_arrive_expect_tx(&bars[fs], bytes);
 #pragma unroll
@@ -515,7 +519,7 @@ __global__ void __launch_bounds__(32 * kQ4DecWarps, 1)
       __syncthreads();
   }
   // after a wait that gave up: the copies still in flight land before the CTA leaves
-  if (!ok && lane == 0) {
+  if (!ok && lane == 0 && !p.stall) {
     for (int s = 0; s < kQ4DecSlots && s < total - done; ++s) {
       const int at = slot + s;
       mbar_wait(&bars[at % kQ4DecSlots], phase ^ (at >= kQ4DecSlots ? 1u : 0u), FAULT_WAIT_FULL);

@@ -1367,7 +1367,7 @@ bool q4_decode_plan(int64_t N, int64_t K, int M, int P, bool copied, int sm_coun
   int64_t best = -1;
   for (int S = 1; S <= 2 && (S == 1 || G >= 8); ++S) {
     const int Gs = ((G + S - 1) / S + 1) & ~1, clusters = std::max(1, sm_count / S);
-    const int64_t x = q4_dec_x_bytes(C, Gs) + q4_dec_f_bytes(C, Gs) + 8 * kQ4DecWarps * kQ4DecSlots;
+    const int64_t x = q4_dec_x_bytes(C, Gs) + q4_dec_f_bytes(C, Gs);
     const int64_t passes = (static_cast<int64_t>(M) * Gs + 8 * kQ4DecWarps - 1) / (8 * kQ4DecWarps);
     for (int Wt = 1; Wt <= kQ4DecWarps; ++Wt) {
       const int Wk = kQ4DecWarps / Wt;
@@ -1377,7 +1377,7 @@ bool q4_decode_plan(int64_t N, int64_t K, int M, int P, bool copied, int sm_coun
       const int64_t nblocks = (N + static_cast<int64_t>(Wt) * rw - 1) / (static_cast<int64_t>(Wt) * rw);
       const int64_t part = q4_dec_part_bytes(C, kQ4DecBoxRows * Wt, Wk);
       const bool once = nblocks <= clusters;  // the partial sums then lie over x'
-      const int64_t rest = 1024 + (once ? std::max(x, part) : x + part);
+      const int64_t rest = 1024 + kQ4DecBarBytes + (once ? std::max(x, part) : x + part);
       const int KB = copied && rest + q4_dec_ring_bytes(2) <= max_smem ? 2 : 1, ring = q4_dec_ring_bytes(KB);
       if (rest + ring > max_smem) continue;
       const int64_t boxes = ((Gs + 2 * KB - 1) / (2 * KB) + Wk - 1) / Wk * KB;
@@ -1386,7 +1386,7 @@ bool q4_decode_plan(int64_t N, int64_t K, int M, int P, bool copied, int sm_coun
       if (best >= 0 && cost >= best) continue;
       best = cost;
       *out = Q4DecodePlan{NT, KB, C, P, rw, static_cast<int>(nblocks), Wt, Wk, S, Gs, clusters,
-                          static_cast<int>(once ? ring : ring + x), static_cast<size_t>(rest + ring)};
+                          static_cast<int>(ring + kQ4DecBarBytes + (once ? 0 : x)), static_cast<size_t>(rest + ring)};
     }
   }
   return best >= 0;
@@ -1428,6 +1428,7 @@ tb_status run_q4_decode(const Q4Args& a, const DevInfo* d, const Q4DecodePlan& p
   p.S = pl.S;
   p.Gs = pl.Gs;
   p.part_at = pl.part_at;
+  p.stall = d->stall.load(std::memory_order_relaxed);
   CUtensorMap tm;
   if (make_map_2d(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.packed, a.K / 2, a.N, a.K / 2, 128,
                   static_cast<uint32_t>(pl.rw), CU_TENSOR_MAP_SWIZZLE_128B) != TB_OK)

@@ -465,3 +465,22 @@ def test_norm_then_ternary_linear(m):
     tb.tb_ternary_linear(rot, tb.TB_FP32, packed, scales, "2bit", m, n, k, None, y[1], tb.TB_FP32, ws, wsb)
     # both are within 2e-3 of the exact product in relative L2
     assert float((y[0] - y[1]).norm() / y[0].norm()) <= 4e-3
+
+
+@pytest.mark.parametrize("m,n,k,xt,signs", [(1, 100, 640, "bf16", False), (1, 17408, 5120, "bf16", False),
+                                            (3, 40000, 1024, "fp16", False), (16, 600, 2048, "bf16", True),
+                                            (16, 5120, 17408, "int8", False)])
+def test_waits_of_the_decode_run_out_and_the_next_call_is_right(m, n, k, xt, signs):
+    """The same for up to 16 tokens: one row block a CTA and several, one CTA and
+    two that split K, a short K whose partial sums reach past the planes of x."""
+    c = Linear(n, m, n, k, xt, k if xt == "int8" else 0, signs, "bf16")
+    tb.tb_get_device_fault(clear=True)
+    tb.tb_test_stall_copies(1, 20_000_000)
+    try:
+        c.run()
+        code = tb.tb_get_device_fault(clear=True)
+    finally:
+        tb.tb_test_stall_copies(0, 0)
+    assert code == 1, code
+    for _ in range(2):
+        c.run().check()
