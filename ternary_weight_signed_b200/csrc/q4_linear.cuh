@@ -48,21 +48,22 @@ __global__ void __launch_bounds__(1024)
   pdl_launch_dependents();
   const int64_t row = blockIdx.x;
   const int tid = threadIdx.x, T = blockDim.x, G = K / 128;
+  const uint32_t k0 = 8 * tid, width = K, step = 8 * T;  // unsigned: k passes K, which may be next to 2^31
   const TIn* xr = x + row * K;
   float f = 1.f;      // x' = x f
   float out_f = 1.f;  // x = x' out_f
   float v[8];
   pdl_wait();
-  if (8 * tid < K) q4_load8<TIn>(xr + 8 * tid, v);
+  if (k0 < width) q4_load8<TIn>(xr + k0, v);
   if (!k8 || group == 128) {
     // the largest magnitude of the row as fp32 bits (NaN and infinity above all)
     uint32_t mb = 0;
     if constexpr (k8) {
       for (int g = tid; g < G; g += T) mb = max(mb, abs_bits(x_scales[row * G + g] * 448.f));
     } else {
-      for (int k = 8 * tid; k < K; k += 8 * T) {
+      for (uint32_t k = k0; k < width; k += step) {
         float u[8];
-        if (k == 8 * tid) {
+        if (k == k0) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) u[i] = v[i];
         } else {
@@ -82,8 +83,8 @@ __global__ void __launch_bounds__(1024)
     out_f = x_scales[row];
   }
   if (tid == 0) factor[row] = out_f;
-  for (int k = 8 * tid; k < K; k += 8 * T) {
-    if (k != 8 * tid) q4_load8<TIn>(xr + k, v);
+  for (uint32_t k = k0; k < width; k += step) {
+    if (k != k0) q4_load8<TIn>(xr + k, v);
     float c = f;
     if constexpr (k8) {
       if (group == 128) c *= x_scales[row * G + (k >> 7)];

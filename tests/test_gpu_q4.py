@@ -484,3 +484,29 @@ def test_waits_of_the_decode_run_out_and_the_next_call_is_right(m, n, k, xt, sig
     assert code == 1, code
     for _ in range(2):
         c.run().check()
+
+
+@pytest.mark.parametrize("xt,group", [("bf16", 0), ("e4m3", 128)])
+def test_the_widest_row(xt, group):
+    """K next to 2^31: nothing wraps on the way.  x is zero but for 2,000 places all over
+    the row, its ends among them, and the scales are 2^-3: every product is exact."""
+    m, n, k = 1, 3, 2 ** 31 - 128
+    g = torch.Generator(device=DEV)
+    g.manual_seed(5)
+    packed = torch.randint(0, 256, (n, k // 2), dtype=torch.uint8, device=DEV, generator=g)
+    scales = torch.full((n, k // 128), 0.125, dtype=torch.float16, device=DEV)
+    at = torch.randint(0, k, (2000,), device=DEV, generator=g)
+    at[:300] = torch.arange(300, device=DEV)
+    at[300:600] = k - 1 - torch.arange(300, device=DEV)
+    at = at.unique()
+    v = torch.randint(-8, 9, at.shape, device=DEV, generator=g).float()
+    x = torch.zeros(m, k, dtype=T[xt][1], device=DEV)
+    x.view(-1)[at] = v.to(x.dtype)
+    xs = torch.ones(m, k // 128, device=DEV) if group else None
+    y = torch.full((m, n), float("nan"), device=DEV)
+    wsb = tb.tb_q4_linear_workspace(m, n, k)
+    ws = torch.empty(wsb, dtype=torch.uint8, device=DEV)
+    tb.tb_q4_linear(x, T[xt][0], xs, group, packed, scales, m, n, k, None, y, tb.TB_FP32, ws, wsb)
+    c = packed[:, at // 2].long()
+    q = torch.where(at % 2 == 0, c & 15, c >> 4).double() - 8.0
+    assert torch.equal(y[0].double(), (q * v.double()).sum(1) * 0.125)
