@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(32 * kPwWarps)
     q4_round_kernel(const TIn* __restrict__ w, uint8_t* __restrict__ packed, uint16_t* __restrict__ scales, int64_t N,
                     int K, bool vec) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int nblk = (K + kHB - 1) / kHB, G = K >> 7;
+  const int nblk = (K - 1) / kHB + 1, G = K >> 7;  // (K + 1023 may pass 2^31)
   const int g0 = static_cast<int>(blockIdx.x % nblk) * 8, ng = min(8, G - g0);
   const int64_t row = static_cast<int64_t>(blockIdx.x / nblk) * kPwWarps + warp;
   if (row >= N) return;

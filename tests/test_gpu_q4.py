@@ -510,3 +510,28 @@ def test_the_widest_row(xt, group):
     c = packed[:, at // 2].long()
     q = torch.where(at % 2 == 0, c & 15, c >> 4).double() - 8.0
     assert torch.equal(y[0].double(), (q * v.double()).sum(1) * 0.125)
+
+
+def test_prepare_the_widest_rows():
+    """Unfolded rows with K next to 2^31, more of them than a block takes: a value
+    here and there, the groups between them zero."""
+    n, k = 9, 2 ** 31 - 128
+    g = torch.Generator(device=DEV)
+    g.manual_seed(6)
+    w = torch.zeros(n, k, dtype=torch.float16, device=DEV)
+    cols = torch.randint(0, k, (300,), device=DEV, generator=g)
+    cols[:2] = torch.tensor([0, k - 1], device=DEV)
+    groups = torch.unique(cols // 128)
+    vals = torch.randn(n, cols.numel(), device=DEV, generator=g).half()
+    w[:, cols] = vals
+    packed = torch.zeros(n, k // 2, dtype=torch.uint8, device=DEV)
+    scales = torch.full((n, k // 128), float("nan"), dtype=torch.float16, device=DEV)
+    tb.tb_q4_prepare_weights(w, tb.TB_FP16, None, n, k, packed, scales)
+    dense = w.view(n, k // 128, 128)[:, groups].reshape(n, -1).double().cpu().numpy()
+    q, s = q4o.prepare_weights(dense)
+    assert np.array_equal(scales[:, groups].cpu().numpy(), s)
+    assert np.array_equal(packed.view(n, k // 128, 64)[:, groups].reshape(n, -1).cpu().numpy(), q4o.pack(q))
+    scales[:, groups] = 0
+    packed.view(n, k // 128, 64)[:, groups] = 0x88
+    for r in range(n):  # a row at a time: the comparisons need memory too
+        assert not scales[r].any() and (packed[r] == 0x88).all()
