@@ -56,10 +56,11 @@ __global__ void __launch_bounds__(1024)
   pdl_wait();
   if (k0 < width) q4_load8<TIn>(xr + k0, v);
   if (!k8 || group == 128) {
-    // the largest magnitude of the row as fp32 bits (NaN and infinity above all)
+    // the largest magnitude of the row, or the largest scale of its groups (their codes
+    // are under 2^9), as fp32 bits (NaN and infinity above all)
     uint32_t mb = 0;
     if constexpr (k8) {
-      for (int g = tid; g < G; g += T) mb = max(mb, abs_bits(x_scales[row * G + g] * 448.f));
+      for (int g = tid; g < G; g += T) mb = max(mb, abs_bits(x_scales[row * G + g]));
     } else {
       for (uint32_t k = k0; k < width; k += step) {
         float u[8];
@@ -75,7 +76,7 @@ __global__ void __launch_bounds__(1024)
     }
     mb = BlockReduce{red, 0}.max_bits(mb);
     // 2^e <= largest < 2^(e+1); a row that holds a NaN or an infinity stays as it is
-    const int top = signs != nullptr ? 9 : 14;
+    const int top = k8 ? 5 : (signs != nullptr ? 9 : 14);
     const int e = mb >= kInfBits ? 0 : max(static_cast<int>(mb >> 23) - 127, -96) - top;
     f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
     out_f = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);

@@ -535,3 +535,15 @@ def test_prepare_the_widest_rows():
     packed.view(n, k // 128, 64)[:, groups] = 0x88
     for r in range(n):  # a row at a time: the comparisons need memory too
         assert not scales[r].any() and (packed[r] == 0x88).all()
+
+
+@pytest.mark.parametrize("m", [3, 16, 17, 60, 130, 300])
+@pytest.mark.parametrize("xt", ["int8", "e4m3"])
+def test_large_scales_of_an_8_bit_row(m, xt):
+    """Finite values near fp32's largest: a scale of 1e36 with codes up to 300."""
+    c = Linear(70, m, 70, 640, xt, 128, False, "fp32")
+    c.scales = (c.scales.astype(np.float32) * 2.0 ** -7).astype(np.float16)  # keeps y finite
+    c.dscales = torch.from_numpy(c.scales.view(np.int16)).to(DEV)
+    c.xs[1] = 1e36
+    c.x[1] = torch.clamp(c.x[1].float(), -300.0, 300.0).to(c.x.dtype)
+    c.run().check()
