@@ -367,16 +367,27 @@ size_t tb_q4_linear_workspace(int64_t M, int64_t N, int64_t K);
  * workspace 16-byte aligned, signs 8 (else TB_ERR_ALIGN).
  * Accuracy: relative L2 error <= 2e-3 and per element <= 1e-2 * max|s| * 8 *
  * ||x_m||_2 before y's own rounding (the figures of tb_ternary_linear, w being
- * up to 8 s here).  Up to 16 tokens the products are exact in a fixed-point x:
- * an int8 x as it is, any other to 2^-22 (up to 5 tokens) or 2^-15 (6 to 16) of
- * its 128-group's largest; past 16 tokens s q and x (scaled by a power of two a
- * row) are rounded to fp16, 2^-11 relative.  Sums are fp32; the same call gives
- * the same bits.  A NaN or an infinity in a row of x, or among its scales, makes
- * that row of y NaN or infinite and touches no other. */
+ * up to 8 s here).  Where tb_q4_linear_path says TB_PATH_GEMV (up to 16 tokens
+ * whose x fits shared memory) the products are exact in a fixed-point x: an int8
+ * x as it is, any other to 2^-22 (up to 5 tokens) or 2^-15 (6 to 16) of its
+ * 128-group's largest.  Else s q and x (scaled by a power of two a row) are
+ * rounded to fp16, 2^-11 relative, which an int8 or e4m3 x with one scale a row
+ * and an unrotated fp16 or bf16 x do not feel (values below 2^-29 of their row's
+ * largest excepted).  Sums are fp32; the same call gives the same bits.  A NaN or
+ * an infinity in a row of x, or among its scales, makes that row of y NaN or
+ * infinite and touches no other. */
 tb_status tb_q4_linear(const void* x, tb_dtype xt, const float* x_scales, int64_t x_group,
                        const uint8_t* packed, const uint16_t* scales, int64_t M, int64_t N, int64_t K,
                        const int8_t* signs, void* y, tb_dtype yt, void* workspace, size_t ws_bytes,
                        void* stream);
+
+/* Which kernels tb_q4_linear takes for these sizes on the current device:
+ * TB_PATH_GEMV, the integer decode kernel, or TB_PATH_GEMM, the tcgen05 kernels;
+ * -1 if it would reject them or the device.  TB_PATH_GEMV holds x in shared
+ * memory: on a B200 always where p M K <= 2^18 and K <= 2^17, p = 1 for int8, 3 for
+ * another type up to 5 tokens, else 2; a little beyond that it depends on N.  (A
+ * 5120-wide x fits up to 16 tokens, a 17408-wide one up to 8, in int8 up to 15.) */
+int tb_q4_linear_path(tb_dtype xt, int64_t M, int64_t N, int64_t K, int has_signs);
 
 /* Read, and with clear != 0 reset, the fault word of the current device.  Every
  * wait inside the library's kernels is bounded; a wait that gives up (a

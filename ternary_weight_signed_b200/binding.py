@@ -50,6 +50,7 @@ _SIGNATURES = {
     "tb_q4_unpack": (_int, [_vp, _i64, _i64, _vp, _vp]),
     "tb_q4_prepare_weights": (_int, [_vp, _int, _vp, _i64, _i64, _vp, _vp, _vp]),
     "tb_q4_linear_workspace": (_sz, [_i64, _i64, _i64]),
+    "tb_q4_linear_path": (_int, [_int, _i64, _i64, _i64, _int]),
     "tb_q4_linear": (_int, [_vp, _int, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _int, _vp, _sz, _vp]),
 }
 
@@ -231,6 +232,10 @@ def tb_q4_prepare_weights(w, wt, signs, n, k, packed, scales, stream=None, check
 
 def tb_q4_linear_workspace(m, n, k) -> int:
     return load().tb_q4_linear_workspace(m, n, k)
+
+
+def tb_q4_linear_path(xt, m, n, k, has_signs=False) -> int:
+    return load().tb_q4_linear_path(xt, m, n, k, int(has_signs))
 
 
 def tb_q4_linear(x, xt, x_scales, x_group, packed, scales, m, n, k, signs, y, yt, workspace, ws_bytes,

@@ -1453,14 +1453,17 @@ tb_status run_q4_decode(const Q4Args& a, const DevInfo* d, const Q4DecodePlan& p
   }
 }
 
+// Whether the decode kernel takes the call, and with what geometry.
+bool q4_decodes(const Q4Args& a, const DevInfo* d, Q4DecodePlan* pl) {
+  if (a.M > kQ4DecMaxM) return false;
+  const int P = q4_planes(a.xt == TB_INT8 ? Q4X_INT8 : Q4X_BF16, static_cast<int>(a.M));
+  const bool copied = a.M > kQ4DecInCta || a.signs != nullptr;
+  return q4_decode_plan(a.N, a.K, static_cast<int>(a.M), P, copied, d->sm_count, d->max_smem_optin, pl);
+}
+
 tb_status run_q4(const Q4Args& a, const DevInfo* d) {
   Q4DecodePlan pl;
-  if (a.M <= kQ4DecMaxM) {
-    const int P = q4_planes(a.xt == TB_INT8 ? Q4X_INT8 : Q4X_BF16, static_cast<int>(a.M));
-    const bool copied = a.M > kQ4DecInCta || a.signs != nullptr;
-    if (q4_decode_plan(a.N, a.K, static_cast<int>(a.M), P, copied, d->sm_count, d->max_smem_optin, &pl))
-      return run_q4_decode(a, d, pl);
-  }
+  if (q4_decodes(a, d, &pl)) return run_q4_decode(a, d, pl);
   if (a.M <= 32) return run_q4_mid<32>(a, d);
   if (a.M <= 64) return run_q4_mid<64>(a, d);
   if (a.M <= 128) return run_q4_mid<128>(a, d);
@@ -1817,6 +1820,20 @@ tb_status tb_q4_linear(const void* x, tb_dtype xt, const float* x_scales, int64_
   st = current_device(&d);
   if (st != TB_OK) return st;
   return run_q4(a, d);
+}
+
+int tb_q4_linear_path(tb_dtype xt, int64_t M, int64_t N, int64_t K, int has_signs) {
+  // a stand-in argument set
+  const uintptr_t base = 0x1000;
+  const bool x8 = is_8bit_dtype(xt);
+  const Q4Args a{reinterpret_cast<const void*>(base), xt, x8 ? reinterpret_cast<const float*>(base) : nullptr,
+                 x8 ? K : 0, reinterpret_cast<const uint8_t*>(base), reinterpret_cast<const uint16_t*>(base), M, N, K,
+                 has_signs ? reinterpret_cast<const int8_t*>(base) : nullptr, reinterpret_cast<void*>(base), TB_FP32,
+                 reinterpret_cast<void*>(base), ~size_t(0), nullptr};
+  const DevInfo* d = nullptr;
+  if (validate_q4(a) != TB_OK || current_device(&d) != TB_OK) return -1;
+  Q4DecodePlan pl;
+  return q4_decodes(a, d, &pl) ? TB_PATH_GEMV : TB_PATH_GEMM;
 }
 
 tb_status tb_test_stall_copies(uint32_t stall, uint64_t wait_limit_ns) {

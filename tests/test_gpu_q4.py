@@ -547,3 +547,113 @@ def test_large_scales_of_an_8_bit_row(m, xt):
     c.xs[1] = 1e36
     c.x[1] = torch.clamp(c.x[1].float(), -300.0, 300.0).to(c.x.dtype)
     c.run().check()
+
+
+# ------------------------------------------------------------------ which kernel, and its accuracy
+PLANES = {"int8": lambda m: 1, "bf16": lambda m: 3 if m <= 5 else 2}
+
+
+def widest(xt, m, n):
+    """The widest K (a multiple of 1024) that the decode kernel takes."""
+    code = T[xt][0]
+    lo, hi = 1024, 1 << 18
+    assert tb.tb_q4_linear_path(code, m, n, lo) == tb.TB_PATH_GEMV
+    if tb.tb_q4_linear_path(code, m, n, hi) == tb.TB_PATH_GEMV:
+        return hi
+    while hi - lo > 1024:
+        mid = (lo + hi) // 2048 * 1024
+        lo, hi = (mid, hi) if tb.tb_q4_linear_path(code, m, n, mid) == tb.TB_PATH_GEMV else (lo, mid)
+    return lo
+
+
+@pytest.mark.parametrize("xt", ["bf16", "fp16", "e4m3", "int8"])
+@pytest.mark.parametrize("n", [1, 5120, 151936])
+def test_path_by_size(xt, n):
+    """The sizes that the header names, and one kernel on either side of one limit."""
+    p, code = tb.tb_q4_linear_path, T[xt][0]
+    for m in range(1, 17):
+        k = min((1 << 18) // (m * PLANES.get(xt, PLANES["bf16"])(m)), 1 << 17) // 128 * 128
+        assert p(code, m, n, k) == p(code, m, n, 128) == p(code, m, n, 5120) == tb.TB_PATH_GEMV
+        w = widest(xt, m, n)
+        assert all(p(code, m, n, w + 1024 * j) == tb.TB_PATH_GEMM for j in (1, 2, 9, 500))
+        assert p(code, m, n, 17408) == (tb.TB_PATH_GEMV if w >= 17408 else tb.TB_PATH_GEMM)
+    assert p(code, 8, n, 17408) == tb.TB_PATH_GEMV and p(code, 17, n, 128) == p(code, 3000, n, 5120) == tb.TB_PATH_GEMM
+    assert xt != "int8" or p(code, 15, n, 17408) == tb.TB_PATH_GEMV
+
+
+class Drawn:
+    """A call on normal x, weights and signs made on the device, its product in 64
+    bits, and what its relative L2 error may be, counted in independent roundings.
+
+    Decode kernel: a value of x is off by at most half a step of its 128-group,
+    uniformly, so y by sqrt(sum_k w^2 step^2 / 12) rms: steps of 2^-21 (three planes) or
+    1.004 2^-14 of the group's largest (two; the higher plane holds 127 of 128), none for
+    an int8.  fp32: a term of 128 products is rounded twice, and at most 160 sums of
+    terms round by 2^-24 / sqrt(3) rms of partial sums that stay under 3 R, R = sqrt(sum
+    w^2 x^2): under 24 2^-24 R.  A rotated x' is off by sqrt(11) 2^-24 of its block's rms.
+    Else: w and (rotated, or with scales per group) x' are rounded to 11 bits, relative
+    errors of at most 2^-11 / sqrt(3) rms each, so sqrt(2/3) 2^-11 R at most.
+    Twice that: with 64 rows of W and more the sum of the errors' squares is within a
+    factor 4 of its mean (its relative deviation is sqrt(2 / 64) at most)."""
+
+    def __init__(self, seed, m, n, k, xt, group=0, signs=False, size=1.0):
+        g = torch.Generator(device=DEV)
+        g.manual_seed(seed)
+        self.m, self.n, self.k, self.xt, self.group = m, n, k, xt, group
+        self.packed = torch.randint(0, 256, (n, k // 2), dtype=torch.uint8, device=DEV, generator=g)
+        self.scales = (torch.rand(n, k // 128, device=DEV, generator=g) * 0.01 + 0.001).to(torch.float16)
+        x = torch.randn(m, k, device=DEV, generator=g)
+        self.xs = None
+        if group:
+            xg = x.view(m, -1, group)
+            self.xs = xg.abs().amax(-1) / (127.0 if xt == "int8" else 448.0)
+            x = (xg / self.xs[..., None]).view(m, k)
+            x = x.round() if xt == "int8" else x.clamp(-448.0, 448.0)
+        self.x = (x * size).to(T[xt][1])
+        self.signs = torch.randint(0, 2, (k,), device=DEV, generator=g).mul(2).sub(1).to(torch.int8) if signs else None
+
+    def run(self):
+        m, n, k = self.m, self.n, self.k
+        y = torch.full((m, n), float("nan"), device=DEV)
+        wsb = tb.tb_q4_linear_workspace(m, n, k)
+        ws = torch.empty(wsb, dtype=torch.uint8, device=DEV)
+        tb.tb_q4_linear(self.x, T[self.xt][0], self.xs, self.group, self.packed, self.scales, m, n, k, self.signs, y,
+                        tb.TB_FP32, ws, wsb)
+        return y
+
+    def check(self):
+        m, n, k = self.m, self.n, self.k
+        x = self.x.double()
+        if self.group:
+            x = x * self.xs.double().repeat_interleave(self.group, 1)
+        if self.signs is not None:
+            x = torch.from_numpy(q4o.orc.rotate(x.cpu().numpy(), self.signs.cpu().numpy())).to(DEV)
+        w = torch.stack((self.packed & 15, self.packed >> 4), -1).view(n, k).double() - 8.0
+        w *= self.scales.double().repeat_interleave(128, 1)
+        ref = x @ w.T
+        w2 = w.square().view(n, -1, 128).sum(-1)  # of a group
+        r2 = float((x.square() @ w.square().T).sum())
+        if tb.tb_q4_linear_path(T[self.xt][0], m, n, k, self.signs is not None) == tb.TB_PATH_GEMV:
+            step = {1: 0.0, 2: 1.004 * 2.0 ** -14, 3: 2.0 ** -21}[PLANES.get(self.xt, PLANES["bf16"])(m)]
+            top = x.abs().view(m, -1, 128).amax(-1)
+            var = float((top.square() @ w2.T).sum()) * step ** 2 / 12.0 + (24 * 2.0 ** -24) ** 2 * r2
+            if self.signs is not None:
+                rms2 = x.square().view(m, -1, 1024).mean(-1).repeat_interleave(8, 1)
+                var += 11 * 2.0 ** -48 * float((rms2 @ w2.T).sum())
+        else:
+            var = r2 * 2.0 / 3.0 * 2.0 ** -22
+        err = float((self.run().double() - ref).norm())
+        assert err <= 2.0 * var ** 0.5, (err, 2.0 * var ** 0.5)
+        assert err <= 2e-3 * float(ref.norm())
+
+
+@pytest.mark.parametrize("m", [3, 5, 9, 16])
+@pytest.mark.parametrize("xt,group,signs", [("bf16", 0, False), ("fp16", 0, True), ("int8", 1, False), ("int8", 128, False),
+                                            ("e4m3", 1, False), ("e4m3", 128, False)])
+def test_accuracy_on_either_side_of_the_limit(m, xt, group, signs):
+    """The widest x that the decode kernel takes, and the next one."""
+    n = 320
+    w = widest(xt, m, n)
+    for i, k in enumerate((w, w + 1024)):
+        assert tb.tb_q4_linear_path(T[xt][0], m, n, k, signs) == (tb.TB_PATH_GEMV, tb.TB_PATH_GEMM)[i]
+        Drawn(k + m, m, n, k, xt, k if group == 1 else group, signs).check()

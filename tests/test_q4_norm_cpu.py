@@ -195,3 +195,11 @@ def test_weights_refusals(lib):
     assert f(FAKE + 2, bf, None, 4, 128, FAKE, FAKE, stream=0, check=False) == tb.TB_ERR_ALIGN
     assert f(FAKE, bf, None, 4, 128, FAKE + 8, FAKE, stream=0, check=False) == tb.TB_ERR_ALIGN
     assert f(FAKE, bf, FAKE + 4, 4, 1024, FAKE, FAKE, stream=0, check=False) == tb.TB_ERR_ALIGN
+
+
+def test_path_rejects(lib):
+    """What the call would refuse has no path (nor has anything without a device)."""
+    p = tb.tb_q4_linear_path
+    for a in ((tb.TB_FP32, 1, 4, 128), (tb.TB_BF16, 0, 4, 128), (tb.TB_BF16, 1, 0, 128), (tb.TB_BF16, 1, 4, 100),
+              (tb.TB_BF16, 1, 4, 128, True), (tb.TB_INT8, 1, 4, 1024, True), (tb.TB_BF16, 2 ** 31, 4, 128)):
+        assert p(*a) == -1
