@@ -657,3 +657,16 @@ def test_accuracy_on_either_side_of_the_limit(m, xt, group, signs):
     for i, k in enumerate((w, w + 1024)):
         assert tb.tb_q4_linear_path(T[xt][0], m, n, k, signs) == (tb.TB_PATH_GEMV, tb.TB_PATH_GEMM)[i]
         Drawn(k + m, m, n, k, xt, k if group == 1 else group, signs).check()
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 17408, 5120), (2, 64, 640), (4, 1024, 5120), (5, 513, 17408), (6, 300, 1024),
+                                   (11, 2049, 5120), (16, 6144, 5120), (16, 5120, 17408), (13, 100, 1152)])
+@pytest.mark.parametrize("xt,group", [("bf16", 0), ("fp16", 0), ("int8", 1), ("int8", 128), ("e4m3", 1), ("e4m3", 128)])
+def test_accuracy_up_to_16_tokens(m, n, k, xt, group):
+    Drawn(n + m, m, n, k, xt, k if group == 1 else group).check()
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 1024, 5120), (4, 640, 2048), (5, 300, 17408), (9, 200, 1024), (16, 6144, 5120)])
+@pytest.mark.parametrize("xt", ["bf16", "fp16"])
+def test_accuracy_of_a_rotated_x(m, n, k, xt):
+    Drawn(n + m, m, n, k, xt, 0, True).check()
