@@ -370,7 +370,7 @@ size_t tb_q4_linear_workspace(int64_t M, int64_t N, int64_t K);
  * up to 8 s here).  Where tb_q4_linear_path says TB_PATH_GEMV (up to 16 tokens
  * whose x fits shared memory) the products are exact in a fixed-point x: an int8
  * x as it is, any other to 2^-22 (up to 5 tokens) or 2^-15 (6 to 16) of its
- * 128-group's largest.  Else s q and x (scaled by a power of two a row) are
+ * 128-group's largest (or of 2^-105 or 2^-112 where that is larger).  Else s q and x (scaled by a power of two a row) are
  * rounded to fp16, 2^-11 relative, which an int8 or e4m3 x with one scale a row
  * and an unrotated fp16 or bf16 x do not feel (values below 2^-29 of their row's
  * largest excepted).  Sums are fp32; the same call gives the same bits.  A NaN or

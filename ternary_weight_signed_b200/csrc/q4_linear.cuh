@@ -75,9 +75,10 @@ __global__ void __launch_bounds__(1024)
       }
     }
     mb = BlockReduce{red, 0}.max_bits(mb);
-    // 2^e <= largest < 2^(e+1); a row that holds a NaN or an infinity stays as it is
+    // x' = x 2^-e: the largest comes to 2^top and more, under 2^(top + 1), or as near
+    // as an fp32 factor takes it; a row that holds a NaN or an infinity stays as it is
     const int top = k8 ? 5 : (signs != nullptr ? 9 : 14);
-    const int e = mb >= kInfBits ? 0 : max(static_cast<int>(mb >> 23) - 127, -96) - top;
+    const int e = mb >= kInfBits ? 0 : max(static_cast<int>(mb >> 23) - 127 - top, -126);
     f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
     out_f = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
   } else {
@@ -193,7 +194,8 @@ __device__ __forceinline__ void q4_store_planes(const float (&v)[32], bool int8,
     mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
     // the largest under 2^22 (three planes) or 1.9921 2^14 (two: the higher one stays under 128)
     const int top = P == 3 ? 21 : 14;
-    const int e = min(max(static_cast<int>((mb + (P == 3 ? 0u : 0x10200u)) >> 23) - 127, -100), 128);
+    // (steps of 2^-126 at least: 1 / step is an fp32 number)
+    const int e = min(max(static_cast<int>((mb + (P == 3 ? 0u : 0x10200u)) >> 23) - 127, top - 126), 128);
     f = __uint_as_float(static_cast<uint32_t>(127 + top - e) << 23);
     inv = mb >= kInfBits ? __uint_as_float(0x7FC00000u) : __uint_as_float(static_cast<uint32_t>(127 - top + e) << 23);
   }

@@ -670,3 +670,10 @@ def test_accuracy_up_to_16_tokens(m, n, k, xt, group):
 @pytest.mark.parametrize("xt", ["bf16", "fp16"])
 def test_accuracy_of_a_rotated_x(m, n, k, xt):
     Drawn(n + m, m, n, k, xt, 0, True).check()
+
+
+@pytest.mark.parametrize("m,signs,size", [(1, False, 1.4e-32), (4, True, 1.4e-32), (7, False, 1.4e-32), (16, True, 1.4e-32),
+                                          (17, True, 1e-37), (64, True, 1e-37), (100, False, 1e-37), (200, True, 1e-37)])
+def test_accuracy_of_tiny_rows(m, signs, size):
+    """bf16 rows near the end of its range keep their bits."""
+    Drawn(m, m, 320, 2048, "bf16", 0, signs, size).check()
