@@ -1268,25 +1268,26 @@ tb_status run_q4_prep(const Q4Args& a, __half* xh, float* factor) {
   }
 }
 
-template <int BT, typename TOut>
+constexpr int kQ4GemmTokens = 256;  // of a tile; up to 128 tokens go to q4_mid_kernel
+
+template <typename TOut>
 tb_status launch_q4_gemm(const Q4Args& a, const DevInfo* d, const CUtensorMap& tm_x, const CUtensorMap& tm_w,
                          const GemmParams& gp, const GemmPairTiles& tl) {
-  auto k = gemm_pair_kernel<BT, TOut, kGpQ4, false>;
+  auto k = gemm_pair_kernel<kQ4GemmTokens, TOut, kGpQ4, false>;
   if (allow_smem(k, d) != TB_OK) return TB_ERR_CUDA;
   // persistent: one cluster per SM pair at most, each walking its tiles
   const int64_t ntiles = static_cast<int64_t>(tl.tiles_n) * tl.tiles_m;
   const dim3 grid(static_cast<unsigned>(2 * std::min<int64_t>(ntiles, std::max(1, d->sm_count / 2))));
-  return launch_pdl(k, grid, dim3(kGpThreads), static_cast<size_t>(gp_smem_bytes(BT, kGpQ4, false)), a.st, tm_x, tm_w,
+  return launch_pdl(k, grid, dim3(kGpThreads), static_cast<size_t>(gp_smem_bytes(kQ4GemmTokens, kGpQ4, false)), a.st, tm_x, tm_w,
                     gp, tl);
 }
 
 tb_status run_q4_gemm(const Q4Args& a, const DevInfo* d) {
   __half* xh = static_cast<__half*>(a.ws);
   float* factor = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + q4_x_bytes(a.M, a.K));
-  const int bt = a.M <= 128 ? 128 : 256;  // as in run_gemm_2bit
   CUtensorMap tm_x, tm_w;
   if (make_map_2d(&tm_x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, xh, a.K, a.M, a.K * 2, gp_atom_k(false),
-                  static_cast<uint32_t>(bt / 2), CU_TENSOR_MAP_SWIZZLE_128B) != TB_OK ||
+                  static_cast<uint32_t>(kQ4GemmTokens / 2), CU_TENSOR_MAP_SWIZZLE_128B) != TB_OK ||
       make_map_2d(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, a.packed, a.K / 8, a.N, a.K / 2,
                   static_cast<uint32_t>(gp_w_row_bytes(kGpQ4, false) / 4), static_cast<uint32_t>(kGpRows),
                   CU_TENSOR_MAP_SWIZZLE_64B) != TB_OK)
@@ -1302,18 +1303,11 @@ tb_status run_q4_gemm(const Q4Args& a, const DevInfo* d) {
   gp.xscale = factor;
   GemmPairTiles tl;
   tl.tiles_n = static_cast<int>((a.N + kGpPairRows - 1) / kGpPairRows);
-  tl.tiles_m = static_cast<int>((a.M + bt - 1) / bt);
-  if (bt == 128) {
-    switch (a.yt) {
-      case TB_FP32: return launch_q4_gemm<128, float>(a, d, tm_x, tm_w, gp, tl);
-      case TB_FP16: return launch_q4_gemm<128, __half>(a, d, tm_x, tm_w, gp, tl);
-      default: return launch_q4_gemm<128, __nv_bfloat16>(a, d, tm_x, tm_w, gp, tl);
-    }
-  }
+  tl.tiles_m = static_cast<int>((a.M + kQ4GemmTokens - 1) / kQ4GemmTokens);
   switch (a.yt) {
-    case TB_FP32: return launch_q4_gemm<256, float>(a, d, tm_x, tm_w, gp, tl);
-    case TB_FP16: return launch_q4_gemm<256, __half>(a, d, tm_x, tm_w, gp, tl);
-    default: return launch_q4_gemm<256, __nv_bfloat16>(a, d, tm_x, tm_w, gp, tl);
+    case TB_FP32: return launch_q4_gemm<float>(a, d, tm_x, tm_w, gp, tl);
+    case TB_FP16: return launch_q4_gemm<__half>(a, d, tm_x, tm_w, gp, tl);
+    default: return launch_q4_gemm<__nv_bfloat16>(a, d, tm_x, tm_w, gp, tl);
   }
 }
 
