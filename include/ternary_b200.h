@@ -280,13 +280,15 @@ tb_status tb_ternary_linear_noalloc(const void* x, tb_dtype xt, const uint8_t* p
 
 /* ------------------------------------------------------------------------
  * Beside the ternary layer: the RMS norm in front of a linear layer and a
- * linear layer with 4-bit weights (for the layers of a ternary model that keep
- * more bits).  The source pages have no counterpart of either; the definitions
- * are this library's own.
+ * linear layer with 4-bit weights, for layers that a user keeps at more bits than
+ * ternary.  The source pages have no counterpart of either; the definitions are
+ * this library's own.
  *
  * 8-bit values with scales: codes a (TB_INT8: -127..127, TB_E4M3) beside fp32
  * scales [M, K / group], row-major, group = K (one a row) or 128 (one per 128
- * consecutive values); a stands for a * scale.
+ * consecutive values); a stands for a * scale.  tb_q4_linear takes both;
+ * tb_ternary_linear's integer mode takes the codes of TB_INT8 and leaves the
+ * scales to the caller.
  * ------------------------------------------------------------------------ */
 
 /* RMS norm of the rows of x [M, K], with the residual's addition in front and
@@ -305,9 +307,10 @@ tb_status tb_ternary_linear_noalloc(const void* x, tb_dtype xt, const uint8_t* p
  *       scale_group 0.  yt in {INT8, E4M3}: with Q = 127 or 448 and per group
  *       scale = max|n| / Q, the code nearest n / scale (ties to even) into y
  *       and the scale into y_scales.  scale_group = K, or 128 where K % 128 == 0
- *       (else TB_ERR_SHAPE).  A group whose largest |n| is below 2^-100 is
- *       stored as scale 0, codes 0.  A group that holds a NaN or an infinity
- *       gets the scale NaN (codes 0 in INT8, NaN in E4M3).
+ *       (else TB_ERR_SHAPE).  The quotient is n times Q / max|n| in fp32: next to a
+ *       border between two codes it may fall on the other side.  A group whose
+ *       largest |n| is below 2^-100 is stored as scale 0, codes 0.  A group that
+ *       holds a NaN or an infinity gets the scale NaN (codes 0 in INT8, NaN in E4M3).
  * xt, rt in {BF16, FP16, FP32}.  Any K from 1 to TB_RMS_NORM_MAX_K; pointers
  * need natural alignment (16 bytes and K % 8 == 0 are faster).  Sums are fp32
  * and do not overflow: a row whose sum of squares does is summed scaled.

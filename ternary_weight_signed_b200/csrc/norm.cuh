@@ -6,8 +6,12 @@
 //   y = n, or per group scale = max|n| / Q and y = round(n / scale).
 //
 // Bound by HBM past a few hundred rows (16384 x 5120, fp32 residual, e4m3 groups:
-// 148 us, 0.96 of the measured copy rate; rotated, 2048 x 5120: 20.2 us, by issue), by
-// the launch and two passes of latency for one (2.7 us).  A row stays in registers between its one load and its one store: a
+// 148 us over one set of buffers, 0.96 of the measured copy rate; 152 to 162 over
+// three), rotated by latency (2048 x 5120: 20.4 us; 20 warps an SM issue in half of the
+// cycles and wait for their rows' copies and the transposes about equally), by the
+// launch and two passes of latency for one row (2.7 us).  Rows over 16384 values go
+// without copies and spill (2048 x 17408 127 us, 0.35 of the copy rate; rotated 137).
+// A row stays in registers between its one load and its one store: a
 // thread holds NV pieces of 8 values (16-byte loads of 16-bit types), a block a
 // row, and the blocks walk the rows.  In the rotated kernel a warp holds a whole
 // 1024-block, so the transform needs no block-wide barrier: distances 1-4, 256 and

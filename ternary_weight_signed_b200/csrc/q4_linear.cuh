@@ -126,8 +126,10 @@ __global__ void __launch_bounds__(1024)
 //     tile in 88 instructions, this one in 24 (1 x 17408 x 5120: 24.1 against 13.7 us
 //     when it replaced it).  tcgen05 wants the codes unpacked to 8 or 16 bits in tensor
 //     memory first; past 16 tokens that pays (q4_mid.cuh).
-//   * One token, 17408 x 5120: 11.3 us a call (0.63 of the measured HBM rate), of which
-//     5 us stream; 151936 x 5120: 78.5 us (0.79).
+//   * One token, 17408 x 5120: 11.3 to 11.8 us a call (0.60 to 0.63 of the measured HBM
+//     rate), of which 5 us stream; 151936 x 5120: 78.9 us (0.79).  bf16 tokens of 17408 x
+//     5120 / 5120 x 17408, us: 2 11.8 / 14.6, 4 15.0 / 18.6, 5 17.3 / 19.1, 8 17.1 / 19.8, 16
+//     24.1 / (q4_mid.cuh, 26.0).
 //   * Each warp streams its own rows: boxes of up to 16 rows x 128 bytes (256
 //     codes) by TMA into a ring of its own, refilled by the warp itself, so no warp
 //     waits for another inside the loop.  K is spread over Wk of a CTA's warps
@@ -138,7 +140,11 @@ __global__ void __launch_bounds__(1024)
 constexpr int kQ4DecWarps = 16;      // of a CTA, one CTA an SM
 constexpr int kQ4DecMaxM = 16;
 constexpr int kQ4DecSlots = 2;       // boxes in flight a warp; 3 and 4 delay the loads of x behind them: 13.0 -> 13.8 us
-constexpr int kQ4DecInCta = 4;       // tokens whose planes every CTA makes itself
+// Tokens whose planes every CTA makes itself; more, and a rotated x, get them from a
+// launch of its own.  In the CTAs / by the launch, us: 1 x 17408 x 5120 11.4 / 13.2, 4 x 15.0 /
+// 16.4, 8 x 17.1 / 17.3; 4 x 5120 x 17408 18.7 / 18.8, 5 x 19.3 / 19.1, 8 x 21.7 / 19.8; int8 8 x
+// 1024 x 5120 7.5 / 6.7.
+constexpr int kQ4DecInCta = 4;
 
 constexpr int kQ4MagicBits = 0x4B400000;   // 1.5 2^23; adding an integer below 2^22 to the bits adds it to the value
 constexpr float kQ4Magic = 12582912.f;

@@ -1148,6 +1148,10 @@ tb_status launch_norm(const NormParams& p, const DevInfo* d, int threads, size_t
 }
 
 // Bulk copies ahead pay from a few rows a block on, when a row is worth a copy.
+// Without / with them, us, e4m3 groups with an fp32 residual: 1184 x 1024 4.7 / 4.9,
+// 1776 x 1024 7.2 / 6.8, 4736 x 1024 14.0 / 12.1, 592 x 5120 11.9 / 11.5, 1184 x 5120 18.3 /
+// 16.4, 4736 x 5120 61.1 / 47.5; 592 x 512 2.4 / 2.9, 4736 x 512 8.4 / 7.2.  Rotated: 1184 x
+// 1024 4.9 / 5.4, 1184 x 5120 18.3 / 12.4 (fewer rows gain too: 592 x 5120 11.5 / 8.2).
 bool norm_bulk(const NormParams& p, const DevInfo* d, size_t smem) {
   return p.vec && p.K >= 1024 && p.M >= 8 * d->sm_count && 2 * (smem + 2048) <= static_cast<size_t>(d->max_smem_optin);
 }
@@ -1161,7 +1165,10 @@ template <int kMode>
 tb_status run_norm_pieces(const NormParams& p, const DevInfo* d, cudaStream_t st) {
   // pieces of a thread: one where a row is alone on its SM (latency), else two, or
   // up to four when the rows come by bulk copies (more bytes in flight a thread,
-  // fewer barriers a byte; without the copies four would spill)
+  // fewer barriers a byte; without the copies four would spill).  One / two pieces
+  // without copies, us: 148 x 5120 3.4 / 5.0, 296 x 5120 6.7 / 6.1, 297 x 5120 8.1 / 6.1, 1000 x
+  // 5120 19.1 / 15.6 (four: 19.0), 1000 x 2048 6.8 / 6.4 but 297 x 2048 3.0 / 4.5, 1000 x 1024
+  // 3.6 / 5.4
   const int pieces = (p.K + 7) / 8 + (kMode == NORM_SHIFTED && p.vec ? 1 : 0);
   const bool many = p.M > 2 * d->sm_count;
   int nv = 1;
@@ -1268,7 +1275,11 @@ tb_status run_q4_prep(const Q4Args& a, __half* xh, float* factor) {
   }
 }
 
-constexpr int kQ4GemmTokens = 256;  // of a tile; up to 128 tokens go to q4_mid_kernel
+// Tokens of a tile.  Up to 128 go to q4_mid_kernel (128 x 17408 x 5120 26.1 us; here 39.6).
+// Past them, with 128-token / 256-token tiles, us: 129 x 17408 x 5120 61.2 / 42.3, 2048 x
+// 17408 x 5120 401 / 276, 385 x 5120 x 17408 181 / 103; where the tiles of both fit the SMs at
+// once the wider one costs up to a tenth: 256 x 1024 x 5120 31.2 / 34.2.
+constexpr int kQ4GemmTokens = 256;
 
 template <typename TOut>
 tb_status launch_q4_gemm(const Q4Args& a, const DevInfo* d, const CUtensorMap& tm_x, const CUtensorMap& tm_w,
